@@ -15,6 +15,9 @@ Operations ("Higher-order Linear Attention" summary, gist.science 2510.27258):
 * :func:`ahla` - asymmetric AHLA (Metodología 2);
 * :func:`hla3` - third-order masked output (Metodología 3).
 
+Beside them, the gated delta rule (:func:`gated_delta`, :func:`gated_delta_step`) and the group norm
+around it (:func:`group_norm`, :func:`group_norm_backward`); see :mod:`.delta`.
+
 Inputs are ``[B, H, T, d]`` (``v``: ``[B, H, T, dv]``) contiguous fp32 or
 bf16 tensors; the output is fp32 ``[B, H, T, dv]``.
 """
@@ -449,3 +452,15 @@ def step(op_name: str, state_io, q, k, v, gamma=None, eps: float = 1e-6, out=Non
     if rc != HLA_OK:
         raise HLAError(rc, "hla_step rejected the call")
     return out
+
+
+_DELTA = ("gated_delta", "gated_delta_step", "gated_delta_workspace_bytes", "group_norm", "group_norm_backward")
+
+
+def __getattr__(name):
+    # the delta module needs torch at import time; the rest of this module imports it when called
+    if name in _DELTA:
+        from . import delta
+        globals().update({n: getattr(delta, n) for n in _DELTA})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

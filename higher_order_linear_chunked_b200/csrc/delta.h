@@ -1,0 +1,49 @@
+// Gated delta rule and group norm: declarations used by their C ABI layer (delta_api.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace hla {
+namespace delta {
+
+// Tokens of one sequence in either layout: element strides of one (b, head, t) row, in rows.
+struct Problem {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const float* state_in;   // [B*H][d][dv] or null
+    const int* lengths;      // [B] or null
+    void* o;
+    float* state_out;        // [B*H][d][dv] or null
+    int B, Hk, H, T, d, dv;
+    bool bf16;
+    bool bthd;
+    float scale;
+};
+
+// Token by token: the state stays in registers, one CTA per head and 64 (or 32) value columns.
+// Used for decoding (T = 1).
+cudaError_t recur(const Problem& p, cudaStream_t st);
+
+}  // namespace delta
+
+namespace gnorm {
+
+struct Args {
+    const void *x, *gate, *dy;
+    const float *weight, *bias;
+    void *y, *dx, *dgate;
+    float *dweight, *dbias, *partial;
+    long long rows;
+    int C, groups, center, silu;
+    float eps;
+};
+
+constexpr int kMaxWidth = 512;   // channels of a group
+
+cudaError_t forward(const Args& a, bool bf16, cudaStream_t st);
+// rows of partial column sums that backward() writes (each 2 C floats)
+int partial_rows(bool bf16, long long rows, int C, int groups);
+cudaError_t backward(const Args& a, bool bf16, cudaStream_t st);
+
+}  // namespace gnorm
+}  // namespace hla
