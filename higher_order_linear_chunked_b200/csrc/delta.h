@@ -20,6 +20,9 @@ struct Problem {
     float scale;
 };
 
+// Chunk by chunk on the tensor cores (delta_forward.cu).
+cudaError_t forward(const Problem& p, cudaStream_t st);
+
 // Token by token: the state stays in registers, one CTA per head and 64 (or 32) value columns.
 // Used for decoding (T = 1).
 cudaError_t recur(const Problem& p, cudaStream_t st);

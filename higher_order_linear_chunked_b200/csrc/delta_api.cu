@@ -67,7 +67,7 @@ hla_status_t hla_delta_forward(const void* q, const void* k, const void* v, cons
     if (workspace_bytes < forward_workspace(dtype, B, Hk, H, T, d, dv)) return HLA_ERR_WORKSPACE;
     const hla::delta::Problem p{q, k, v, g, beta, state_in, lengths, o, state_out, B, Hk, H, T, d, dv,
                                 dtype == HLA_BF16, layout == HLA_BTHD, scale};
-    return hla::delta::recur(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
+    return hla::delta::forward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
 
 hla_status_t hla_delta_step(float* state, const void* q, const void* k, const void* v, const float* g,
