@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace hla {
 namespace delta {
@@ -20,8 +21,13 @@ struct Problem {
     float scale;
 };
 
-// Chunk by chunk on the tensor cores (delta_forward.cu).
-cudaError_t forward(const Problem& p, cudaStream_t st);
+// Chunk by chunk on the tensor cores (delta_forward.cu), with forward_bytes() of workspace.
+size_t forward_bytes(const Problem& p);
+cudaError_t forward(const Problem& p, void* ws, cudaStream_t st);
+
+// The chunks' records (delta_prepare.cu); gradients: the form that the backward pass reads.
+size_t records_bytes(const Problem& p, bool gradients);
+cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st);
 
 // Token by token: the state stays in registers, one CTA per head and 64 (or 32) value columns.
 // Used for decoding (T = 1).

@@ -33,7 +33,12 @@ hla_status_t check_norm(hla_dtype_t dtype, long long rows, int C, int groups, in
     return HLA_OK;
 }
 
-size_t forward_workspace(hla_dtype_t, int, int, int, int, int, int) { return hla::kStatusBytes; }
+size_t forward_workspace(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
+    hla::delta::Problem p{};
+    p.bf16 = dtype == HLA_BF16;
+    p.B = B; p.Hk = Hk; p.H = H; p.T = T; p.d = d; p.dv = dv;
+    return hla::kStatusBytes + hla::delta::forward_bytes(p);
+}
 
 }  // namespace
 
@@ -47,7 +52,7 @@ size_t hla_delta_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T,
 }
 
 int hla_delta_kernel_launches(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
-    return check_shape(dtype, B, Hk, H, T, d, dv) == HLA_OK ? 1 : 0;
+    return check_shape(dtype, B, Hk, H, T, d, dv) == HLA_OK ? 2 : 0;
 }
 
 hla_status_t hla_delta_forward(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -67,7 +72,8 @@ hla_status_t hla_delta_forward(const void* q, const void* k, const void* v, cons
     if (workspace_bytes < forward_workspace(dtype, B, Hk, H, T, d, dv)) return HLA_ERR_WORKSPACE;
     const hla::delta::Problem p{q, k, v, g, beta, state_in, lengths, o, state_out, B, Hk, H, T, d, dv,
                                 dtype == HLA_BF16, layout == HLA_BTHD, scale};
-    return hla::delta::forward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
+    void* body = static_cast<char*>(workspace) + hla::kStatusBytes;
+    return hla::delta::forward(p, body, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
 
 hla_status_t hla_delta_step(float* state, const void* q, const void* k, const void* v, const float* g,

@@ -6,9 +6,9 @@
 //     U = diag(beta) R
 //     O = scale diag(e^c) Q S0 + P U
 //     S = e^(c_C) S0 + K^T diag(e^(c_C - c)) U
-// A block owns CS = 16 NG value columns of one head (S's columns do not mix).  Two warps hold the
-// state of 16 columns transposed in registers, half of the key axis each, so S^T, Y^T and U^T are
-// in turn the A operand of the next product and only the partial K S0 passes through shared memory.
+// A block owns CS = 16 NG value columns of one head (S's columns do not mix).  NH warps hold the
+// state of 16 columns transposed in registers, each a part of the key axis; between the products
+// they share the chunk's Y and U, each splitting the tokens of its part once, through shared memory.
 #include "delta_walk.cuh"
 
 namespace hla {
@@ -19,7 +19,7 @@ enum Mode { OUT = 0, SUMMARY = 1, STORE = 2 };
 
 struct WalkArgs {
     const void *q, *k, *v;
-    const float *g, *beta;
+    const uint8_t* records;   // [BH][chunks][record], see delta_walk.cuh
     const float* start;       // states before each segment [BH][segments][d][dv], or one per head, or null
     const int* lengths;
     void* o;
@@ -39,39 +39,40 @@ struct Cfg {
     static constexpr int KT = BF ? 1 : 3;             // terms of q, k
     static constexpr int OT = BF ? 2 : 3;             // terms of S0, U and P in the outputs: twice the
                                                       // 8 bits that a bf16 output keeps
-    static constexpr bool PIPE = BF || DK_ < 128;     // fp32 at d = 128 has no room for that
-    static constexpr int NST = PIPE ? (BF ? 6 : 5) : 2;
-    static constexpr int NLD = BF ? 1 : 4;            // loader warps (fp32 tiles are split on the way)
-    static constexpr int W_STATE = 2 * NG_, W_OUT = 2, W_PROD = 2;
-    static constexpr int WARPS = W_STATE + W_OUT + W_PROD + 1 + NLD;
+    static constexpr int INV = MODE_ == STORE ? 2 : 1, PT = MODE_ == STORE ? 3 : OT;   // the records' form
+    static constexpr int AHEAD = BF ? 3 : 1;          // chunks between a tile's request and its use
+    static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
+    static constexpr int NH = DK_ == 32 ? 2 : 4;      // state warps of 16 columns
+    static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? 2 * NG_ : 0;
+    static constexpr int WARPS = W_STATE + W_OUT + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2;
-    static constexpr int VTILE = cols_bytes<E, CS>();
-    static constexpr int NP = PIPE ? 4 : 1, N2 = PIPE ? 2 : 1;
-    // shared memory, bytes
-    static constexpr int k = 0;
-    static constexpr int q = k + NST * KTILE;
-    static constexpr int v = q + (MODE_ == OUT ? NST * KTILE : 0);
-    static constexpr int gates = v + NST * VTILE;
-    static constexpr int m = gates + NST * static_cast<int>(sizeof(Gates));
-    static constexpr int p = m + N2 * C * kMS * 4;
-    static constexpr int PB = OT * C * C * 2;
-    static constexpr int x = p + (MODE_ == OUT ? NP * PB : 0);
-    static constexpr int XB = 3 * C * C * 2;
-    static constexpr int sf = x + N2 * XB;
+    // ring of AHEAD + 1 stages: keys, inverse, values
+    static constexpr int NS = AHEAD + 1;
+    static constexpr int k = 0, x = k + KTILE, v = x + kXBytes;
+    static constexpr int STAGE = (v + cols_bytes<E, CS>() + 255) / 256 * 256;
+    // ring of AHEAD + 2: gates, and for the outputs, a chunk behind, queries and P
+    static constexpr int NO = AHEAD + 2;
+    static constexpr int PB = PT * C * C * 2;
+    static constexpr int behind = NS * STAGE;
+    static constexpr int gates = 0, q = 512, p = q + KTILE;
+    static constexpr int OSTAGE = MODE_ == OUT ? p + PB : 512;
+    // S0 and U of the last two chunks for the outputs, the partial sums
+    static constexpr int sf = behind + NO * OSTAGE;
     static constexpr int SB = NG_ * (DK_ / 16) * OT * 512;
-    static constexpr int uf = sf + (MODE_ == OUT ? N2 * SB : 0);
+    static constexpr int uf = sf + (MODE_ == OUT ? 2 * SB : 0);
     static constexpr int UB = NG_ * 2 * OT * 512;
-    static constexpr int ex = uf + (MODE_ == OUT ? N2 * UB : 0);
-    static constexpr int bytes = ex + W_STATE * 2048;
+    static constexpr int ex = uf + (MODE_ == OUT ? 2 * UB : 0);
+    static constexpr int yf = ex + W_STATE * 2048;    // Y of the chunk as an A operand; the decayed U
+    static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
+    static constexpr int bytes = yf + NG_ * YB;
 };
 
 template <typename F>
 __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs a) {
     using E = typename F::Elem;
-    constexpr int DK = F::DK, DH = DK / 2, NG = F::NG, CS = F::CS, KT = F::KT, OT = F::OT;
-    constexpr bool PIPE = F::PIPE;
+    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, NG = F::NG, CS = F::CS, KT = F::KT, OT = F::OT;
     constexpr Mode MODE = F::MODE;
-    extern __shared__ __align__(128) uint8_t sm[];
+    extern __shared__ __align__(1024) uint8_t sm[];   // swizzles are exclusive ors of address bits
     const uint32_t sb = ptx::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -95,12 +96,12 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
     const long long vrow = row_of(a.bthd, b, h, a.H, t_first, a.T);
 
     // roles
-    const int w_out = F::W_STATE, w_prod = w_out + F::W_OUT, w_inv = w_prod + F::W_PROD, w_load = w_inv + 1;
-    const int grp = warp >> 1, half = warp & 1;                 // state warps
+    constexpr int w_out = F::W_STATE, w_load = w_out + F::W_OUT;
+    const int grp = warp / NH, part = warp % NH;                // state warps
     float S[DH / 8][4];
     if (warp < F::W_STATE) {
         // S^T: this lane's columns col, col + 8, keys 8 n + 2 (lane % 4), + 1 of its half
-        const int col = col0 + 16 * grp + (lane >> 2), key = half * DH + 2 * (lane & 3);
+        const int col = col0 + 16 * grp + (lane >> 2), key = part * DH + 2 * (lane & 3);
         const float* from = nullptr;
         if (a.start && !unit && (MODE != SUMMARY || seg == 0))
             from = a.start + (MODE == SUMMARY ? bh : static_cast<long long>(bh) * a.segments + seg) * DK * a.dv;
@@ -112,227 +113,261 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
                 S[n][j] = unit ? (kk == cc ? 1.f : 0.f) : (from ? from[static_cast<long long>(kk) * a.dv + cc] : 0.f);
             }
     }
-    float next_g = 0.f, next_beta = 0.f;
-
-    const int s0 = -4, s1 = PIPE ? chunks : 4 * chunks - 1;
-    if (chunks > 0)
-    for (int s = s0; s <= s1; ++s) {
-        if (warp < F::W_STATE) {
-            // ------------------------------------------------ state
-            const int c = chunk_of<PIPE>(s, 0, 2);
-            if (c >= 0 && c < chunks) {
-                const int st = c % F::NST, c2 = c % F::N2;
-                const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates) + st;
-                const uint32_t kt = sb + F::k + st * F::KTILE, vt = sb + F::v + st * F::VTILE;
-                const uint32_t xt = sb + F::x + c2 * F::XB;
-                uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + c2 * F::SB);
-                uint4* uf = reinterpret_cast<uint4*>(sm + F::uf + c2 * F::UB);
-                float y[4][4] = {};
-                // this half's part of S0^T K^T
+    // Step s: tiles of chunk s + AHEAD asked for, state over chunk s, outputs of chunk s - 1; one
+    // barrier of the whole block a step, each role in a loop of its own.
+    constexpr int ALL = F::WARPS * 32;
+    const auto step_end = [] { ptx::named_sync(15, ALL); };
+    if (chunks > 0 && warp < F::W_STATE) {
+        // ---------------------------------------------------- state
+        // this lane's places in a stage's keys and inverse
+        const uint32_t k_n = at_pieces_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
+        const uint32_t k_t = at_rows_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
+        float4* const ex = reinterpret_cast<float4*>(sm + F::ex) + grp * NH * 128 + lane;
+        uint8_t* const yf = sm + F::yf + grp * F::YB;
+        uint8_t* const vf = reinterpret_cast<uint8_t*>(ex - lane);
+        int stage = 0, ostage = 0;
+        for (int s = -F::AHEAD; s < 0; ++s) step_end();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t so = stage * F::STAGE;
+            const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + ostage * F::OSTAGE + F::gates);
+            uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 16) + part * (DH / 16)) * OT * 32 + lane;
+            uint2* uf = reinterpret_cast<uint2*>(sm + F::uf + (c & 1) * F::UB) + grp * 2 * OT * 64 + lane * 2;
+            // this part's share of S0^T K^T, all tokens
+            float y[4][4] = {};
 #pragma unroll
-                for (int ks = 0; ks < DH / 16; ++ks) {
-                    uint32_t as[3][4];
-                    split_a<3>(S[2 * ks], S[2 * ks + 1], as);
-                    if (MODE == OUT) {
+            for (int ks = 0; ks < DH / 16; ++ks) {
+                uint32_t bk[2][KT][4];
 #pragma unroll
-                        for (int t = 0; t < OT; ++t)
-                            sf[((grp * (DK / 16) + half * (DH / 16) + ks) * OT + t) * 32 + lane] =
-                                make_uint4(as[t][0], as[t][1], as[t][2], as[t][3]);
-                    }
+                for (int np = 0; np < 2; ++np)
 #pragma unroll
-                    for (int np = 0; np < 2; ++np) {
-                        uint32_t bk[KT][4];
+                    for (int t = 0; t < KT; ++t)   // a step of 16 keys changes the piece by two: its swizzle is an exclusive or
+                        ldsm4(bk[np][t], ((k_n + so) ^ (ks << 5)) + t * (C * DK * 2) + np * 16 * DK * 2);
+                uint32_t as[3][4];
+                split_a<3>(S[2 * ks], S[2 * ks + 1], as);
+                prod<3, KT, 2>(y, as, bk);
+                if (MODE == OUT) {
 #pragma unroll
-                        for (int t = 0; t < KT; ++t)
-                            ldsm4(bk[t], at_pieces_first<DK * 2>(kt + t * (C * DK * 2), 16 * np, half * (DH / 8) + 2 * ks, lane));
-                        prod2<3, KT>(y[2 * np], y[2 * np + 1], as, bk);
-                    }
+                    for (int t = 0; t < OT; ++t) sf[(ks * OT + t) * 32] = make_uint4(as[t][0], as[t][1], as[t][2], as[t][3]);
                 }
-                float4* ex = reinterpret_cast<float4*>(sm + F::ex);
+            }
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    ex[((grp * 2 + half) * 4 + n) * 32 + lane] = make_float4(y[n][0], y[n][1], y[n][2], y[n][3]);
-                ptx::named_sync(1 + grp, 64);
-                // Y^T = V^T - (S0^T K^T) e^c
+            for (int n = 0; n < 4; ++n)
+                if (n / TN != part) ex[(part * 4 + n) * 32] = make_float4(y[n][0], y[n][1], y[n][2], y[n][3]);
+            // meanwhile: V, gates and the inverse for the tokens of this part
+            float v[2][4] = {};
+            if (!unit) cols_t<CS>(static_cast<const E*>(nullptr), sb + F::v + so, 16 * grp, part * TN * 8 / 16 * 16, lane, v[0], v[1]);
+            float2 since[TN], beta[TN], left[TN];
+            uint32_t bx[TN][3][4];
 #pragma unroll
-                for (int np = 0; np < 2; ++np) {
-                    float v0[4] = {}, v1[4] = {};
-                    if (!unit) cols_t<CS>(static_cast<const E*>(nullptr), vt, 16 * grp, 16 * np, lane, v0, v1);
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e, tok = 8 * n + 2 * (lane & 3);
+                since[e] = *reinterpret_cast<const float2*>(&G->since[tok]);
+                beta[e] = *reinterpret_cast<const float2*>(&G->beta[tok]);
+                left[e] = *reinterpret_cast<const float2*>(&G->left[tok]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int n = 2 * np + e;
-                        const float4 o = ex[((grp * 2 + (half ^ 1)) * 4 + n) * 32 + lane];
-                        const float2 f = *reinterpret_cast<const float2*>(&G->since[8 * n + 2 * (lane & 3)]);
-                        const float (&vv)[4] = e ? v1 : v0;
-                        y[n][0] = fmaf(-f.x, y[n][0] + o.x, vv[0]);
-                        y[n][1] = fmaf(-f.y, y[n][1] + o.y, vv[1]);
-                        y[n][2] = fmaf(-f.x, y[n][2] + o.z, vv[2]);
-                        y[n][3] = fmaf(-f.y, y[n][3] + o.w, vv[3]);
-                    }
+                for (int t = 0; t < 3; ++t)
+                    ldsm4(bx[e][t], sb + F::x + so + t * (C * C * 2) + piece<C * 2>(8 * n + (lane & 7), lane >> 3));
+            }
+            const float all = G->all;
+            float mine[TN][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)                   // (register arrays take constant indexes only)
+                if (n / TN == part)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mine[n % TN][j] = y[n][j];
+            ptx::named_sync(1 + grp, NH * 32);
+            // Y^T = V^T - (S0^T K^T) e^c for the tokens of this part
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e;
+                float w[4] = {mine[e][0], mine[e][1], mine[e][2], mine[e][3]};
+#pragma unroll
+                for (int o = 1; o < NH; ++o) {
+                    const float4 x = ex[((part ^ o) * 4 + n) * 32];
+                    w[0] += x.x; w[1] += x.y; w[2] += x.z; w[3] += x.w;
                 }
-                // R^T = Y^T X^T, X lower triangular: tokens 16.. of the sum reach tokens 16.. alone
+                float z[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float vv = TN == 2 ? v[e][j] : ((part & 1) ? v[1][j] : v[0][j]);
+                    z[j] = fmaf((j & 1) ? -since[e].y : -since[e].x, w[j], vv);
+                }
+                uint32_t t0[3], t1[3];
+                split<3>(z[0], z[1], t0);
+                split<3>(z[2], z[3], t1);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    reinterpret_cast<uint2*>(yf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
+            }
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[n][j] *= all;
+            ptx::named_sync(1 + grp, NH * 32);
+            // R^T = Y^T X^T for the tokens of this part; X is lower triangular
+            uint32_t ay[2][3][4];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint4 u = reinterpret_cast<const uint4*>(yf)[(kk * 3 + t) * 32 + lane];
+                    ay[kk][t][0] = u.x; ay[kk][t][1] = u.y; ay[kk][t][2] = u.z; ay[kk][t][3] = u.w;
+                }
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e;
                 float r[4][4] = {};
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t ay[3][4];
-                    split_a<3>(y[2 * kk], y[2 * kk + 1], ay);
+                for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int np = kk; np < 2; ++np) {
-                        uint32_t bx[3][4];
-#pragma unroll
-                        for (int t = 0; t < 3; ++t) ldsm4(bx[t], at_pieces_first<C * 2>(xt + t * (C * C * 2), 16 * np, 2 * kk, lane));
-                        prod2<3, 3>(r[2 * np], r[2 * np + 1], ay, bx);
+                    for (int j = 0; j < 3 - i; ++j) {
+                        mma16816(r[(i + j) & 1], ay[0][i], bx[e][j][0], bx[e][j][1]);
+                        if (n >= 2) mma16816(r[2 + ((i + j) & 1)], ay[1][i], bx[e][j][2], bx[e][j][3]);
                     }
-                }
-                // U^T, for the outputs, and U^T e^(c_C - c), for the state
+                // U^T for the outputs, and U^T e^(c_C - c) for the state
+                float u[4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 be = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
-                    r[n][0] *= be.x; r[n][1] *= be.y; r[n][2] *= be.x; r[n][3] *= be.y;
-                }
+                for (int j = 0; j < 4; ++j) u[j] = ((r[0][j] + r[1][j]) + (r[2][j] + r[3][j])) * ((j & 1) ? beta[e].y : beta[e].x);
+                uint32_t t0[3], t1[3];
+                split<3>(u[0] * left[e].x, u[1] * left[e].y, t0);
+                split<3>(u[2] * left[e].x, u[3] * left[e].y, t1);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    reinterpret_cast<uint2*>(vf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
                 if (MODE == OUT) {
-                    uint32_t au[OT][4];
-                    if (half == 0) split_a<OT>(r[0], r[1], au);
-                    else split_a<OT>(r[2], r[3], au);
+                    uint32_t o0[OT], o1[OT];
+                    split<OT>(u[0], u[1], o0);
+                    split<OT>(u[2], u[3], o1);
 #pragma unroll
-                    for (int t = 0; t < OT; ++t)
-                        uf[((grp * 2 + half) * OT + t) * 32 + lane] = make_uint4(au[t][0], au[t][1], au[t][2], au[t][3]);
+                    for (int t = 0; t < OT; ++t) uf[((n >> 1) * OT + t) * 64 + (n & 1)] = make_uint2(o0[t], o1[t]);
                 }
+            }
+            uint32_t bt[2][DH / 16][KT][4];
+            if constexpr (KT == 1) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 f = *reinterpret_cast<const float2*>(&G->left[8 * n + 2 * (lane & 3)]);
-                    r[n][0] *= f.x; r[n][1] *= f.y; r[n][2] *= f.x; r[n][3] *= f.y;
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int np = 0; np < DH / 16; ++np)
+                        ldsm4t(bt[kk][np][0], ((k_t + so) ^ (np << 5)) + kk * 16 * DK * 2);
+            }
+            ptx::named_sync(1 + grp, NH * 32);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t au[3][4];
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint4 u = reinterpret_cast<const uint4*>(vf)[(kk * 3 + t) * 32 + lane];
+                    au[t][0] = u.x; au[t][1] = u.y; au[t][2] = u.z; au[t][3] = u.w;
                 }
-                const float all = G->all;
+                if constexpr (KT > 1) {
 #pragma unroll
-                for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[n][j] *= all;
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t au[3][4];
-                    split_a<3>(r[2 * kk], r[2 * kk + 1], au);
-#pragma unroll
-                    for (int np = 0; np < DH / 16; ++np) {
-                        uint32_t bk[KT][4];
+                    for (int np = 0; np < DH / 16; ++np)
 #pragma unroll
                         for (int t = 0; t < KT; ++t)
-                            ldsm4t(bk[t], at_rows_first<DK * 2>(kt + t * (C * DK * 2), 16 * kk, half * (DH / 8) + 2 * np, lane));
-                        prod2<3, KT>(S[2 * np], S[2 * np + 1], au, bk);
-                    }
+                            ldsm4t(bt[kk][np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                }
+                prod<3, KT, DH / 16>(S, au, bt[kk]);
+            }
+            if (++stage == F::NS) stage = 0;
+            if (++ostage == F::NO) ostage = 0;
+            step_end();
+        }
+        step_end();
+    } else if (chunks > 0 && warp < w_load) {
+        // ---------------------------------------------------- output: 16 tokens of 16 columns a warp
+        const int i0 = 16 * ((warp - w_out) & 1), g = (warp - w_out) >> 1;
+        const uint32_t q_a = at_rows_first<DK * 2>(sb + F::behind + F::q, i0, 0, lane);
+        const uint32_t p_a = at_rows_first<C * 2>(sb + F::behind + F::p, i0, 0, lane);
+        const int r0 = i0 + (lane >> 2);
+        E* o = static_cast<E*>(a.o) + (vrow + static_cast<long long>(r0) * vstep) * a.dv + col0 + 16 * g + 2 * (lane & 3);
+        const long long next8 = static_cast<long long>(8) * vstep * a.dv;
+        int ostage = 0;
+        for (int s = -F::AHEAD; s < 1; ++s) step_end();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t so = ostage * F::OSTAGE;
+            const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + so + F::gates);
+            const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 16) * OT * 32 + lane;
+            const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + (c & 1) * F::UB) + g * 2 * OT * 32 + lane;
+            float acc[2][2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                uint32_t aq[KT][4], bs[1][OT][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t) ldsm4(aq[t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2));
+#pragma unroll
+                for (int t = 0; t < OT; ++t) {
+                    const uint4 u = sf[(ks * OT + t) * 32];
+                    bs[0][t][0] = u.x; bs[0][t][1] = u.z; bs[0][t][2] = u.y; bs[0][t][3] = u.w;
+                }
+                prod<KT, OT, 1>(acc[ks & 1], aq, bs);
+            }
+            const float f[2] = {a.scale * G->since[r0], a.scale * G->since[r0 + 8]};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[0][n][j] = (acc[0][n][j] + acc[1][n][j]) * f[j >> 1];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                if (kk == 1 && i0 == 0) continue;
+                uint32_t ap[OT][4], bu[1][OT][4];
+#pragma unroll
+                for (int t = 0; t < OT; ++t) {
+                    ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2));
+                    const uint4 u = uf[(kk * OT + t) * 32];
+                    bu[0][t][0] = u.x; bu[0][t][1] = u.z; bu[0][t][2] = u.y; bu[0][t][3] = u.w;
+                }
+                prod<OT, OT, 1>(acc[0], ap, bu);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = t_first + c * C + r0 + 8 * e;
+                if (tok >= t_last) continue;
+                const bool on = tok < t_end;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float x0 = on ? acc[0][n][2 * e] : 0.f, x1 = on ? acc[0][n][2 * e + 1] : 0.f;
+                    if constexpr (F::BF) *reinterpret_cast<uint32_t*>(o + e * next8 + 8 * n) = ptx::pack_bf16(x0, x1);
+                    else *reinterpret_cast<float2*>(o + e * next8 + 8 * n) = make_float2(x0, x1);
                 }
             }
-        } else if (warp < w_prod) {
-            // ------------------------------------------------ output: 16 tokens a warp
-            const int c = chunk_of<PIPE>(s, -1, 3);
-            if (MODE == OUT && c >= 0 && c < chunks) {
-                const int st = c % F::NST, c2 = c % F::N2, i0 = 16 * (warp - w_out);
-                const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates) + st;
-                const uint32_t qt = sb + F::q + st * F::KTILE, pt = sb + F::p + (c % F::NP) * F::PB;
-                const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + c2 * F::SB);
-                const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + c2 * F::UB);
-                float acc[2 * NG][4] = {};
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    uint32_t aq[KT][4];
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) ldsm4(aq[t], at_rows_first<DK * 2>(qt + t * (C * DK * 2), i0, 2 * ks, lane));
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        uint32_t bs[OT][4];
-#pragma unroll
-                        for (int t = 0; t < OT; ++t) {
-                            const uint4 u = sf[((g * (DK / 16) + ks) * OT + t) * 32 + lane];
-                            bs[t][0] = u.x; bs[t][1] = u.z; bs[t][2] = u.y; bs[t][3] = u.w;
-                        }
-                        prod2<KT, OT>(acc[2 * g], acc[2 * g + 1], aq, bs);
-                    }
-                }
-                const int r0 = i0 + (lane >> 2);
-                const float f0 = a.scale * G->since[r0], f1 = a.scale * G->since[r0 + 8];
-#pragma unroll
-                for (int n = 0; n < 2 * NG; ++n) {
-                    acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
-                }
-                for (int kk = 0; kk <= warp - w_out; ++kk) {
-                    uint32_t ap[OT][4];
-#pragma unroll
-                    for (int t = 0; t < OT; ++t) ldsm4(ap[t], at_rows_first<C * 2>(pt + t * (C * C * 2), i0, 2 * kk, lane));
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        uint32_t bu[OT][4];
-#pragma unroll
-                        for (int t = 0; t < OT; ++t) {
-                            const uint4 u = uf[((g * 2 + kk) * OT + t) * 32 + lane];
-                            bu[t][0] = u.x; bu[t][1] = u.z; bu[t][2] = u.y; bu[t][3] = u.w;
-                        }
-                        prod2<OT, OT>(acc[2 * g], acc[2 * g + 1], ap, bu);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = c * C + r0 + 8 * e;              // within the segment
-                    if (t_first + tok >= t_last) continue;
-                    const bool on = t_first + tok < t_end;
-                    E* o = static_cast<E*>(a.o) + (vrow + static_cast<long long>(tok) * vstep) * a.dv + col0 + 2 * (lane & 3);
-#pragma unroll
-                    for (int n = 0; n < 2 * NG; ++n) {
-                        const float x0 = on ? acc[n][2 * e] : 0.f, x1 = on ? acc[n][2 * e + 1] : 0.f;
-                        if constexpr (F::BF) *reinterpret_cast<uint32_t*>(o + 8 * n) = ptx::pack_bf16(x0, x1);
-                        else *reinterpret_cast<float2*>(o + 8 * n) = make_float2(x0, x1);
-                    }
-                }
-            }
-        } else if (warp < w_inv) {
-            // ------------------------------------------------ products
-            const int c = chunk_of<PIPE>(s, 2, 0);
-            if (c >= 0 && c < chunks) {
-                const int st = c % F::NST;
-                products<DK, KT, OT, MODE == OUT, false>(
-                    sb + F::k + st * F::KTILE, sb + F::q + st * F::KTILE, reinterpret_cast<const Gates*>(sm + F::gates) + st,
-                    reinterpret_cast<float*>(sm + F::m) + (c % F::N2) * C * kMS, sm + F::p + (c % F::NP) * F::PB, a.scale,
-                    warp - w_prod, lane);
-            }
-        } else if (warp < w_load) {
-            // ------------------------------------------------ inverse
-            const int c = chunk_of<PIPE>(s, 1, 1);
-            if (c >= 0 && c < chunks)
-                invert(reinterpret_cast<const float*>(sm + F::m) + (c % F::N2) * C * kMS, sm + F::x + (c % F::N2) * F::XB, lane);
-        } else {
-            // ------------------------------------------------ load: bf16 tiles are asked for four chunks
-            // ahead and there three ahead; fp32 tiles are loaded and split three ahead
-            const int lt = (warp - w_load) * 32 + lane;
-            constexpr int LT = F::NLD * 32;
-            const int c = PIPE ? (F::BF ? s + 4 : s + 3) : ((s & 3) == 0 ? (s >> 2) + 1 : -1);
-            const float g_was = next_g, beta_was = next_beta;
-            if (c >= 0 && c < chunks) {
-                const int st = c % F::NST, rows = min(C, t_end - t_first - c * C);
-                const long long kr = krow + static_cast<long long>(c) * C * kstep, vr = vrow + static_cast<long long>(c) * C * vstep;
-                const long long ks = static_cast<long long>(kstep) * DK, vs = static_cast<long long>(vstep) * a.dv;
-                load_tile<DK, KT, LT>(sb + F::k + st * F::KTILE, static_cast<const E*>(a.k) + kr * DK, ks, rows, lt);
-                if (MODE == OUT) load_tile<DK, KT, LT>(sb + F::q + st * F::KTILE, static_cast<const E*>(a.q) + kr * DK, ks, rows, lt);
-                if (!unit) load_cols<CS, LT>(sb + F::v + st * F::VTILE, static_cast<const E*>(a.v) + vr * a.dv + col0, vs, rows, lt);
-                if (warp == w_load) {
-                    const bool on = lane < rows;
-                    next_g = on ? a.g[vr + static_cast<long long>(lane) * vstep] : 0.f;
-                    next_beta = on ? a.beta[vr + static_cast<long long>(lane) * vstep] : 0.f;
-                    if (!(PIPE && F::BF)) finish_gates(reinterpret_cast<Gates*>(sm + F::gates) + st, next_g, next_beta, lane);
-                }
+            o += 4 * next8;
+            if (++ostage == F::NO) ostage = 0;
+            step_end();
+        }
+    } else if (chunks > 0) {
+        // ---------------------------------------------------- load
+        const int lt = (warp - w_load) * 32 + lane;
+        constexpr int LT = F::NLD * 32;
+        const long long ks = static_cast<long long>(kstep) * DK, vs = static_cast<long long>(vstep) * a.dv;
+        const E* kp = static_cast<const E*>(a.k) + krow * DK;
+        const E* qp = static_cast<const E*>(a.q) + krow * DK;
+        const E* vp = static_cast<const E*>(a.v) + vrow * a.dv + col0;
+        const uint8_t* rec = a.records + (static_cast<long long>(bh) * ((a.T + C - 1) / C) + t_first / C) *
+                                             record_bytes(F::INV, F::PT);
+        int stage = 0, ostage = 0;
+        for (int c = 0; c <= chunks + F::AHEAD; ++c) {
+            if (c < chunks) {
+                const uint32_t sg = sb + stage * F::STAGE, so = sb + F::behind + ostage * F::OSTAGE;
+                const int rows = min(C, t_end - t_first - c * C);
+                load_bytes<kXBytes, LT>(sg + F::x, rec, lt);
+                if (MODE == OUT) load_bytes<F::PB, LT>(so + F::p, rec + F::INV * kXBytes, lt);
+                load_bytes<512, LT>(so + F::gates, rec + F::INV * kXBytes + F::PB, lt);
+                if (!unit) load_cols<CS, LT>(sg + F::v, vp, vs, rows, lt);
+                load_tile<DK, KT, LT>(sg + F::k, kp, ks, rows, lt);
+                if (MODE == OUT) load_tile<DK, KT, LT>(so + F::q, qp, ks, rows, lt);
+                kp += C * ks; qp += C * ks; vp += C * vs;
+                rec += record_bytes(F::INV, F::PT);
+                if (++stage == F::NS) stage = 0;
+                if (++ostage == F::NO) ostage = 0;
             }
             cp_commit();
-            if constexpr (PIPE && F::BF) {
-                cp_wait<1>();
-                if (c - 1 >= 0 && c - 1 < chunks)
-                    finish_gates(reinterpret_cast<Gates*>(sm + F::gates) + (c - 1) % F::NST, g_was, beta_was, lane);
-            } else {
-                cp_wait<0>();
-            }
+            cp_wait<F::AHEAD - 1>();
+            step_end();
         }
-        __syncthreads();
     }
 
     if (warp < F::W_STATE) {
-        const int col = col0 + 16 * grp + (lane >> 2), key = half * DH + 2 * (lane & 3);
+        const int col = col0 + 16 * grp + (lane >> 2), key = part * DH + 2 * (lane & 3);
         float* to = nullptr;
         long long width = a.dv;
         if (MODE == SUMMARY) {
@@ -366,27 +401,32 @@ cudaError_t start(const WalkArgs& a, int blocks, cudaStream_t st) {
 }
 
 template <typename E, int DK>
-cudaError_t walk(const Problem& p, cudaStream_t st) {
+cudaError_t walk(const Problem& p, void* ws, cudaStream_t st) {
     constexpr int NG = sizeof(E) == 2 ? 2 : 1;
     using F = Cfg<E, DK, NG, OUT>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const int BH = p.B * p.H, NC = (p.T + C - 1) / C;
-    WalkArgs a{p.q, p.k, p.v, p.g, p.beta, p.state_in, p.lengths, p.o, p.state_out, nullptr,
+    uint8_t* records = static_cast<uint8_t*>(ws);
+    cudaError_t e = prepare(p, false, records, st);
+    if (e != cudaSuccess) return e;
+    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, p.o, p.state_out, nullptr,
                p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, 1, NC, p.scale};
     return start<F>(a, BH * (p.dv / F::CS), st);
 }
 
 }  // namespace
 
-cudaError_t forward(const Problem& p, cudaStream_t st) {
+size_t forward_bytes(const Problem& p) { return records_bytes(p, false); }
+
+cudaError_t forward(const Problem& p, void* ws, cudaStream_t st) {
     if (p.bf16) {
-        if (p.d == 32) return walk<bf16, 32>(p, st);
-        if (p.d == 64) return walk<bf16, 64>(p, st);
-        return walk<bf16, 128>(p, st);
+        if (p.d == 32) return walk<bf16, 32>(p, ws, st);
+        if (p.d == 64) return walk<bf16, 64>(p, ws, st);
+        return walk<bf16, 128>(p, ws, st);
     }
-    if (p.d == 32) return walk<float, 32>(p, st);
-    if (p.d == 64) return walk<float, 64>(p, st);
-    return walk<float, 128>(p, st);
+    if (p.d == 32) return walk<float, 32>(p, ws, st);
+    if (p.d == 64) return walk<float, 64>(p, ws, st);
+    return walk<float, 128>(p, ws, st);
 }
 
 }  // namespace delta

@@ -18,7 +18,7 @@ namespace delta {
 constexpr int C = 32;   // tokens of a chunk
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -38,15 +38,32 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// acc[0] += A B(n-tile 0), acc[1] += A B(n-tile 1), b[t] = {tile 0 k-low, k-high, tile 1 k-low, k-high}
+// c[n] += A B(n-tile n) for 2 NP tiles; b[np][t] = {tile 2 np k-low, k-high, tile 2 np + 1 k-low, k-high}.
+// The tiles of one pair of terms follow one another, so a tile's own chain of sums does not stall
+// them, and the leading terms come first: they are ready before the residuals are.
+template <int AT, int BT, int NP>
+__device__ __forceinline__ void prod(float (&c)[2 * NP][4], const uint32_t (&a)[AT][4], const uint32_t (&b)[NP][BT][4]) {
+    constexpr int M = AT > BT ? AT : BT;
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int j = 0; j < BT; ++j)
+            if (i + j < M) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    mma16816(c[2 * p], a[i], b[p][j][0], b[p][j][1]);
+                    mma16816(c[2 * p + 1], a[i], b[p][j][2], b[p][j][3]);
+                }
+            }
+}
 template <int AT, int BT>
 __device__ __forceinline__ void prod2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[AT][4],
                                       const uint32_t (&b)[BT][4]) {
     constexpr int M = AT > BT ? AT : BT;
 #pragma unroll
-    for (int i = AT - 1; i >= 0; --i)
+    for (int i = 0; i < AT; ++i)
 #pragma unroll
-        for (int j = BT - 1; j >= 0; --j)
+        for (int j = 0; j < BT; ++j)
             if (i + j < M) {
                 mma16816(c0, a[i], b[j][0], b[j][1]);
                 mma16816(c1, a[i], b[j][2], b[j][3]);

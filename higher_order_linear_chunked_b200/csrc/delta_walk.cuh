@@ -1,9 +1,7 @@
-// Roles shared by the forward and the reverse walk of the gated delta rule: the loader, the
-// decayed products K K^T and Q K^T of a chunk, and the inverse of its unit triangular system.
-//
-// A block walks the chunks (32 tokens) of one head for CS value columns, a warp or two to a role,
-// each role one chunk ahead of the next, one block barrier a step:
-//     load (c)  ->  products (c)  ->  inverse (c)  ->  state (c)  ->  output (c)
+// Pieces of the gated delta rule's chunk kernels: what a chunk needs that does not depend on the
+// carried state (its decayed products, the inverse of its unit triangular system, its gate values:
+// a record in the workspace, written by delta_prepare.cu for all chunks at once), and the loaders
+// of the kernels that walk the chunks.
 #pragma once
 #include "delta_mma.cuh"
 
@@ -12,21 +10,27 @@ namespace delta {
 
 constexpr int kMS = 36;                      // floats of a row of the transposed system
 
-// Values of a chunk's decays: c = sum of g up to the token as hi + lo (differences of two such
-// sums keep 2^-24 of the gap however large the sums are), e^c, e^(c_last - c), beta.
+// Gate values of a chunk: e^c, e^(c_last - c), beta, e^(c_last); c = sum of g up to the token.
 struct Gates {
-    float2 sum[C];
     float since[C], left[C], beta[C];
-    float all;                               // e^(c_last)
-    float pad[3];
+    float all;
+    float pad[31];
 };
+static_assert(sizeof(Gates) == 512, "a record's last piece");
 
-// Which chunk a role works on in step s: PIPE, each role `ahead` of the state's chunk s; else the
-// roles take turns, four steps a chunk.
-template <bool PIPE>
-__device__ __forceinline__ int chunk_of(int s, int ahead, int turn) {
-    if constexpr (PIPE) return s + ahead;
-    return (s & 3) == turn ? (s >> 2) : -1;
+// Bytes of a chunk's record: `inverses` three-term inverses, P in PT terms, the gates.
+constexpr int kXBytes = 3 * C * C * 2;
+constexpr int record_bytes(int inverses, int PT) { return inverses * kXBytes + PT * C * C * 2 + 512; }
+
+__device__ __forceinline__ float ex2(float x) {      // 2^x to 2^-22
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^x, the whole part apart from the rest: a rounding of a large x costs nothing
+__device__ __forceinline__ float ex2_long(double x) {
+    const float n = rintf(static_cast<float>(x));
+    return ex2(static_cast<float>(x - static_cast<double>(n))) * ex2(n);
 }
 
 // 32 rows of D elements into KT swizzled bf16 tiles, by NT threads; rows >= `rows` become zeros.
@@ -34,10 +38,12 @@ template <int D, int KT, int NT>
 __device__ __forceinline__ void load_tile(uint32_t tile, const bf16* src, long long step, int rows, int tid) {
     static_assert(KT == 1, "bf16 inputs are one term");
     constexpr int P = D / 8;
-    for (int i = tid; i < C * P; i += NT) {
-        const int r = i / P, c = i % P;
+    const int c = tid % P;
+    src += c * 8;
+#pragma unroll 4
+    for (int r = tid / P; r < C; r += NT / P) {
         const bool on = r < rows;
-        cp_async16(tile + piece<D * 2>(r, c), src + (on ? r * step : 0) + c * 8, on);
+        cp_async16(tile + piece<D * 2>(r, c), src + (on ? r * step : 0), on);
     }
 }
 template <int D, int KT, int NT>
@@ -45,6 +51,7 @@ __device__ __forceinline__ void load_tile(uint32_t tile, const float* src, long 
     constexpr int P = D / 4;                  // four floats at a time
     constexpr int N = (C * P + NT - 1) / NT;
     constexpr int U = N < 8 ? N : 8;
+#pragma unroll 1
     for (int base = 0; base < N; base += U) {
         float4 x[U];
 #pragma unroll
@@ -87,6 +94,12 @@ __device__ __forceinline__ void load_cols(uint32_t tile, const float* src, long 
         cp_async16(tile + (r * (CS + 4) + c * 4) * 4, src + (on ? r * step : 0) + c * 4, on);
     }
 }
+// N bytes as they are (a record's piece), by NT threads.
+template <int N, int NT>
+__device__ __forceinline__ void load_bytes(uint32_t to, const uint8_t* src, int tid) {
+#pragma unroll 4
+    for (int i = tid; i < N / 16; i += NT) cp_async16(to + i * 16, src + i * 16, true);
+}
 template <typename E, int CS>
 constexpr int cols_bytes() { return sizeof(E) == 2 ? C * CS * 2 : C * (CS + 4) * 4; }
 
@@ -118,9 +131,11 @@ __device__ __forceinline__ void cols_t(const float*, uint32_t tile, int col0, in
     }
 }
 
-// Gate values of one chunk from each lane's g and beta (lane = token; idle tokens: 0 and 0).
-__device__ __forceinline__ void finish_gates(Gates* s, float g, float beta, int lane) {
-    double c = gate(g);
+// Gate values of one chunk from each lane's g and beta (lane = token; idle tokens: 0 and 0), and
+// sum[i] = c_i / ln 2 as hi + lo: the difference of two such sums keeps 2^-24 of the gap however
+// large the sums are.
+__device__ __forceinline__ void finish_gates(Gates* s, float2* sum, float g, float beta, int lane) {
+    double c = static_cast<double>(gate(g)) * 1.4426950408889634;   // 1 / ln 2
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
         const double o = __shfl_up_sync(0xffffffffu, c, w);
@@ -128,58 +143,63 @@ __device__ __forceinline__ void finish_gates(Gates* s, float g, float beta, int 
     }
     const double last = __shfl_sync(0xffffffffu, c, 31);
     const float hi = static_cast<float>(c);
-    s->sum[lane] = make_float2(hi, static_cast<float>(c - static_cast<double>(hi)));
-    s->since[lane] = expf(hi);
-    s->left[lane] = expf(static_cast<float>(last - c));
+    sum[lane] = make_float2(hi, static_cast<float>(c - static_cast<double>(hi)));
+    const float since = ex2_long(c);
+    s->since[lane] = since;
+    s->left[lane] = ex2_long(last - c);
     s->beta[lane] = beta;
-    if (lane == 31) s->all = expf(hi);
+    s->pad[lane < 31 ? lane : 30] = 0.f;
+    if (lane == 31) s->all = since;
 }
 
-// Products of a chunk, warp p of two: rows 16p.. of M = strict_low(D o K K^T) with a beta factor, to
-// mt[j][i] (transposed), and of P = scale low(D o Q K^T) as PT bf16 terms.  ROWBETA: beta_i, else beta_j.
-template <int DK, int KT, int PT, bool QUERY, bool ROWBETA>
-__device__ __forceinline__ void products(uint32_t kt, uint32_t qt, const Gates* s, float* mt, uint8_t* pt, float scale,
-                                         int p, int lane) {
+// 16 rows (16p..) of a chunk's decayed products with the keys, one warp.
+//   keys:  M = strict_low(D o K K^T) with a beta factor (rowbeta: beta_i, else beta_j), to mt[j][i]
+//   else:  P = scale low(D o Q K^T) as PT bf16 terms, to pt
+template <int DK, int KT, int PT>
+__device__ __forceinline__ void products(bool keys, bool rowbeta, uint32_t kt, uint32_t at, const float2* sum, const float* beta,
+                                         float* mt, uint8_t* pt, float scale, int p, int lane) {
     constexpr int RB = DK * 2, TERM = C * DK * 2;
-    float kk[4][4] = {}, qk[4][4] = {};
-#pragma unroll
+    float acc[4][4] = {};
+#pragma unroll(DK > 32 ? 2 : 1)
     for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t a[KT][4], aq[KT][4];
+        uint32_t a[KT][4];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            ldsm4(a[t], at_rows_first<RB>(kt + t * TERM, 16 * p, 2 * ks, lane));
-            if (QUERY) ldsm4(aq[t], at_rows_first<RB>(qt + t * TERM, 16 * p, 2 * ks, lane));
-        }
+        for (int t = 0; t < KT; ++t) ldsm4(a[t], at_rows_first<RB>(at + t * TERM, 16 * p, 2 * ks, lane));
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
             if (np > p) continue;
             uint32_t b[KT][4];
 #pragma unroll
             for (int t = 0; t < KT; ++t) ldsm4(b[t], at_pieces_first<RB>(kt + t * TERM, 16 * np, 2 * ks, lane));
-            prod2<KT, KT>(kk[2 * np], kk[2 * np + 1], a, b);
-            if (QUERY) prod2<KT, KT>(qk[2 * np], qk[2 * np + 1], aq, b);
+            prod2<KT, KT>(acc[2 * np], acc[2 * np + 1], a, b);
         }
+    }
+    float2 ci[2];
+    float fi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = 16 * p + (lane >> 2) + 8 * h;
+        ci[h] = sum[i];
+        fi[h] = keys ? (rowbeta ? beta[i] : 1.f) : scale;
     }
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         if (nt > 2 * p + 1) continue;
+        const int j0 = 8 * nt + 2 * (lane & 3);
+        const float4 cj = *reinterpret_cast<const float4*>(&sum[j0]);
+        float2 fj = make_float2(1.f, 1.f);
+        if (!rowbeta && keys) fj = *reinterpret_cast<const float2*>(&beta[j0]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int i = 16 * p + (lane >> 2) + 8 * h, j0 = 8 * nt + 2 * (lane & 3);
-            const float2 ci = s->sum[i];
-            const float bi = s->beta[i];
-            float pr[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = j0 + e;
-                const float2 cj = s->sum[j];
-                const float D = j <= i ? expf((ci.x - cj.x) + (ci.y - cj.y)) : 0.f;
-                mt[j * kMS + i] = j < i ? D * kk[nt][2 * h + e] * (ROWBETA ? bi : s->beta[j]) : 0.f;
-                pr[e] = j <= i ? scale * D * qk[nt][2 * h + e] : 0.f;
-            }
-            if (QUERY) {
+            const int i = 16 * p + (lane >> 2) + 8 * h;
+            const float x0 = fi[h] * fj.x * acc[nt][2 * h] * ex2((ci[h].x - cj.x) + (ci[h].y - cj.y));
+            const float x1 = fi[h] * fj.y * acc[nt][2 * h + 1] * ex2((ci[h].x - cj.z) + (ci[h].y - cj.w));
+            if (keys) {
+                mt[j0 * kMS + i] = j0 < i ? x0 : 0.f;
+                mt[(j0 + 1) * kMS + i] = j0 + 1 < i ? x1 : 0.f;
+            } else {
                 uint32_t t[PT];
-                split<PT>(pr[0], pr[1], t);
+                split<PT>(j0 <= i ? x0 : 0.f, j0 + 1 <= i ? x1 : 0.f, t);
 #pragma unroll
                 for (int n = 0; n < PT; ++n)
                     *reinterpret_cast<uint32_t*>(pt + n * (C * C * 2) + piece<C * 2>(i, j0 >> 3) + (j0 & 7) * 2) = t[n];
@@ -188,34 +208,75 @@ __device__ __forceinline__ void products(uint32_t kt, uint32_t qt, const Gates* 
     }
 }
 
-// X = (I + L)^-1 of the strictly lower L (mt[j][i] = L_ij), column `lane` by forward substitution
-// in fp32, to three bf16 terms [i][j].
+// X = (I + L)^-1 of the strictly lower L (mt[j][i] = L_ij) as three bf16 terms [i][j], one warp.
+// The two 16 x 16 blocks on the diagonal by forward substitution in fp32, a column a lane; below
+// them X21 = -X22 L21 X11 in two products of three-term operands, transposed so that the first
+// one's accumulators are the second one's A operand.
 __device__ __forceinline__ void invert(const float* mt, uint8_t* xt, int lane) {
-    float x[C];
+    constexpr int TERM = C * C * 2;
+    const int blk = lane >> 4, col = lane & 15;
+    const float* m = mt + 16 * blk * (kMS + 1);
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < C; ++i) x[i] = i == lane ? 1.f : 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < C - 1; ++j) {
+    for (int j = 0; j < 15; ++j) {
 #pragma unroll
-        for (int i4 = (j + 1) / 4 * 4; i4 < C; i4 += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(mt + j * kMS + i4);
-            if (i4 + 0 > j) x[i4 + 0] = fmaf(-m.x, x[j], x[i4 + 0]);
-            if (i4 + 1 > j) x[i4 + 1] = fmaf(-m.y, x[j], x[i4 + 1]);
-            if (i4 + 2 > j) x[i4 + 2] = fmaf(-m.z, x[j], x[i4 + 2]);
-            if (i4 + 3 > j) x[i4 + 3] = fmaf(-m.w, x[j], x[i4 + 3]);
+        for (int i4 = (j + 1) / 4 * 4; i4 < 16; i4 += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(m + j * kMS + i4);
+            if (i4 + 0 > j) x[i4 + 0] = fmaf(-f.x, x[j], x[i4 + 0]);
+            if (i4 + 1 > j) x[i4 + 1] = fmaf(-f.y, x[j], x[i4 + 1]);
+            if (i4 + 2 > j) x[i4 + 2] = fmaf(-f.z, x[j], x[i4 + 2]);
+            if (i4 + 3 > j) x[i4 + 3] = fmaf(-f.w, x[j], x[i4 + 3]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < C; i += 2) {
+    for (int i = 0; i < 16; i += 2) {
         uint32_t t[3];
         split<3>(x[i], x[i + 1], t);
 #pragma unroll
         for (int n = 0; n < 3; ++n) {
-            uint8_t* q = xt + n * (C * C * 2) + (lane & 7) * 2;
-            *reinterpret_cast<uint16_t*>(q + piece<C * 2>(i, lane >> 3)) = static_cast<uint16_t>(t[n]);
-            *reinterpret_cast<uint16_t*>(q + piece<C * 2>(i + 1, lane >> 3)) = static_cast<uint16_t>(t[n] >> 16);
+            uint8_t* q = xt + n * TERM + (lane & 7) * 2;
+            *reinterpret_cast<uint16_t*>(q + piece<C * 2>(16 * blk + i, lane >> 3)) = static_cast<uint16_t>(t[n]);
+            *reinterpret_cast<uint16_t*>(q + piece<C * 2>(16 * blk + i + 1, lane >> 3)) = static_cast<uint16_t>(t[n] >> 16);
         }
     }
+    __syncwarp();
+    const uint32_t xb = ptx::smem_u32(xt);
+    // Z^T [col][i] = X11^T L21^T
+    uint32_t a[3][4], b[3][4];
+#pragma unroll
+    for (int t = 0; t < 3; ++t)   // X11 is stored [j][col]: transposed 8 x 8 blocks, rows of A = columns
+        ldsm4t(a[t], xb + t * TERM + piece<C * 2>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {  // n-tile n >> 1, k half n & 1
+        const float* l = mt + (2 * (lane & 3) + 8 * (n & 1)) * kMS + 16 + 8 * (n >> 1) + (lane >> 2);
+        uint32_t t[3];
+        split<3>(-l[0], -l[kMS], t);
+        b[0][n] = t[0]; b[1][n] = t[1]; b[2][n] = t[2];
+    }
+    float z[2][4] = {};
+    prod2<3, 3>(z[0], z[1], a, b);
+    // X21^T [col][i] = -Z^T X22^T
+    split_a<3>(z[0], z[1], a);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) ldsm4(b[t], at_pieces_first<C * 2>(xb + t * TERM, 16, 2, lane));
+    float y[2][4] = {};
+    prod2<3, 3>(y[0], y[1], a, b);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c0 = (lane >> 2) + 8 * h, i = 16 + 8 * n + 2 * (lane & 3);
+            uint32_t t[3];
+            split<3>(y[n][2 * h], y[n][2 * h + 1], t);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                uint8_t* q = xt + k * TERM + (c0 & 7) * 2;
+                *reinterpret_cast<uint16_t*>(q + piece<C * 2>(i, c0 >> 3)) = static_cast<uint16_t>(t[k]);
+                *reinterpret_cast<uint16_t*>(q + piece<C * 2>(i + 1, c0 >> 3)) = static_cast<uint16_t>(t[k] >> 16);
+            }
+        }
 }
 
 }  // namespace delta
