@@ -42,8 +42,8 @@ struct Cfg {
     static constexpr int INV = MODE_ == STORE ? 2 : 1, PT = MODE_ == STORE ? 3 : OT;   // the records' form
     static constexpr int AHEAD = BF ? 3 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
-    static constexpr int NH = DK_ == 32 ? 2 : 4;      // state warps of 16 columns
-    static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? 2 * NG_ : 0;
+    static constexpr int NH = DK_ == 128 ? 4 : 2;     // state warps of 16 columns
+    static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? NG_ : 0;
     static constexpr int WARPS = W_STATE + W_OUT + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2;
     // ring of AHEAD + 1 stages: keys, inverse, values
@@ -70,7 +70,7 @@ struct Cfg {
 template <typename F>
 __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs a) {
     using E = typename F::Elem;
-    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, NG = F::NG, CS = F::CS, KT = F::KT, OT = F::OT;
+    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, CS = F::CS, KT = F::KT, OT = F::OT;
     constexpr Mode MODE = F::MODE;
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzles are exclusive ors of address bits
     const uint32_t sb = ptx::smem_u32(sm);
@@ -274,12 +274,11 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
         }
         step_end();
     } else if (chunks > 0 && warp < w_load) {
-        // ---------------------------------------------------- output: 16 tokens of 16 columns a warp
-        const int i0 = 16 * ((warp - w_out) & 1), g = (warp - w_out) >> 1;
-        const uint32_t q_a = at_rows_first<DK * 2>(sb + F::behind + F::q, i0, 0, lane);
-        const uint32_t p_a = at_rows_first<C * 2>(sb + F::behind + F::p, i0, 0, lane);
-        const int r0 = i0 + (lane >> 2);
-        E* o = static_cast<E*>(a.o) + (vrow + static_cast<long long>(r0) * vstep) * a.dv + col0 + 16 * g + 2 * (lane & 3);
+        // ---------------------------------------------------- output: 16 columns a warp
+        const int g = warp - w_out;
+        const uint32_t q_a = at_rows_first<DK * 2>(sb + F::behind + F::q, 0, 0, lane);
+        const uint32_t p_a = at_rows_first<C * 2>(sb + F::behind + F::p, 0, 0, lane);
+        E* o = static_cast<E*>(a.o) + (vrow + static_cast<long long>(lane >> 2) * vstep) * a.dv + col0 + 16 * g + 2 * (lane & 3);
         const long long next8 = static_cast<long long>(8) * vstep * a.dv;
         int ostage = 0;
         for (int s = -F::AHEAD; s < 1; ++s) step_end();
@@ -288,44 +287,53 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
             const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + so + F::gates);
             const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 16) * OT * 32 + lane;
             const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + (c & 1) * F::UB) + g * 2 * OT * 32 + lane;
-            float acc[2][2][4] = {};
+            float acc[2][2][4] = {};          // [16 tokens][8 columns]
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
-                uint32_t aq[KT][4], bs[1][OT][4];
-#pragma unroll
-                for (int t = 0; t < KT; ++t) ldsm4(aq[t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2));
+                uint32_t aq[2][KT][4], bs[1][OT][4];
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
                     const uint4 u = sf[(ks * OT + t) * 32];
                     bs[0][t][0] = u.x; bs[0][t][1] = u.z; bs[0][t][2] = u.y; bs[0][t][3] = u.w;
                 }
-                prod<KT, OT, 1>(acc[ks & 1], aq, bs);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) ldsm4(aq[m][t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2) + m * 16 * DK * 2);
+                    prod<KT, OT, 1>(acc[m], aq[m], bs);
+                }
             }
-            const float f[2] = {a.scale * G->since[r0], a.scale * G->since[r0 + 8]};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int m = 0; m < 2; ++m) {
+                const float f[2] = {a.scale * G->since[16 * m + (lane >> 2)], a.scale * G->since[16 * m + 8 + (lane >> 2)]};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[0][n][j] = (acc[0][n][j] + acc[1][n][j]) * f[j >> 1];
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[m][n][j] *= f[j >> 1];
+            }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                if (kk == 1 && i0 == 0) continue;
                 uint32_t ap[OT][4], bu[1][OT][4];
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
-                    ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2));
                     const uint4 u = uf[(kk * OT + t) * 32];
                     bu[0][t][0] = u.x; bu[0][t][1] = u.z; bu[0][t][2] = u.y; bu[0][t][3] = u.w;
                 }
-                prod<OT, OT, 1>(acc[0], ap, bu);
+#pragma unroll
+                for (int m = kk; m < 2; ++m) {     // P is lower triangular
+#pragma unroll
+                    for (int t = 0; t < OT; ++t) ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2) + m * 16 * C * 2);
+                    prod<OT, OT, 1>(acc[m], ap, bu);
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tok = t_first + c * C + r0 + 8 * e;
+            for (int e = 0; e < 4; ++e) {
+                const int tok = t_first + c * C + (lane >> 2) + 8 * e;
                 if (tok >= t_last) continue;
                 const bool on = tok < t_end;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float x0 = on ? acc[0][n][2 * e] : 0.f, x1 = on ? acc[0][n][2 * e + 1] : 0.f;
+                    const float x0 = on ? acc[e >> 1][n][2 * (e & 1)] : 0.f, x1 = on ? acc[e >> 1][n][2 * (e & 1) + 1] : 0.f;
                     if constexpr (F::BF) *reinterpret_cast<uint32_t*>(o + e * next8 + 8 * n) = ptx::pack_bf16(x0, x1);
                     else *reinterpret_cast<float2*>(o + e * next8 + 8 * n) = make_float2(x0, x1);
                 }
