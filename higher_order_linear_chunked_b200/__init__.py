@@ -15,7 +15,8 @@ Operations ("Higher-order Linear Attention" summary, gist.science 2510.27258):
 * :func:`ahla` - asymmetric AHLA (Metodología 2);
 * :func:`hla3` - third-order masked output (Metodología 3).
 
-Beside them, the gated delta rule (:func:`gated_delta`, :func:`gated_delta_step`) and the group norm
+Beside them, the gated delta rule (:func:`gated_delta`, :func:`gated_delta_step`,
+:func:`gated_delta_backward`) and the group norm
 around it (:func:`group_norm`, :func:`group_norm_backward`); see :mod:`.delta`.
 
 Inputs are ``[B, H, T, d]`` (``v``: ``[B, H, T, dv]``) contiguous fp32 or
@@ -454,7 +455,8 @@ def step(op_name: str, state_io, q, k, v, gamma=None, eps: float = 1e-6, out=Non
     return out
 
 
-_DELTA = ("gated_delta", "gated_delta_step", "gated_delta_workspace_bytes", "group_norm", "group_norm_backward")
+_DELTA = ("gated_delta", "gated_delta_step", "gated_delta_backward", "gated_delta_workspace_bytes",
+          "gated_delta_backward_workspace_bytes", "group_norm", "group_norm_backward")
 
 
 def __getattr__(name):

@@ -29,6 +29,23 @@ cudaError_t forward(const Problem& p, void* ws, cudaStream_t st);
 size_t records_bytes(const Problem& p, bool gradients);
 cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st);
 
+// The forward walk for the gradients: the state before each block of block_chunks chunks
+// [BH][blocks][d][dv] and each token's error R [BH][T][dv]; records in the gradients' form.
+cudaError_t store_states(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
+                         cudaStream_t st);
+
+// Gradients (delta_backward.cu).  dstate_out: the gradient at the last state, or null; dstate_in: the
+// one at the first state, or null when it is not wanted.
+struct Gradients {
+    const void* dout;
+    const float* dstate_out;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dstate_in;
+};
+size_t backward_bytes(const Problem& p);
+int backward_launches(const Problem& p);
+cudaError_t backward(const Problem& p, const Gradients& gr, void* ws, cudaStream_t st);
+
 // Token by token: the state stays in registers, one CTA per head and 64 (or 32) value columns.
 // Used for decoding (T = 1).
 cudaError_t recur(const Problem& p, cudaStream_t st);

@@ -33,11 +33,15 @@ hla_status_t check_norm(hla_dtype_t dtype, long long rows, int C, int groups, in
     return HLA_OK;
 }
 
-size_t forward_workspace(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
+hla::delta::Problem sizes(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
     hla::delta::Problem p{};
     p.bf16 = dtype == HLA_BF16;
     p.B = B; p.Hk = Hk; p.H = H; p.T = T; p.d = d; p.dv = dv;
-    return hla::kStatusBytes + hla::delta::forward_bytes(p);
+    return p;
+}
+
+size_t forward_workspace(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
+    return hla::kStatusBytes + hla::delta::forward_bytes(sizes(dtype, B, Hk, H, T, d, dv));
 }
 
 }  // namespace
@@ -88,6 +92,43 @@ hla_status_t hla_delta_step(float* state, const void* q, const void* k, const vo
     const hla::delta::Problem p{q, k, v, g, beta, state, nullptr, o, state, B, Hk, H, 1, d, dv,
                                 dtype == HLA_BF16, false, scale};
     return hla::delta::recur(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
+}
+
+size_t hla_delta_backward_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
+    if (check_shape(dtype, B, Hk, H, T, d, dv) != HLA_OK) return 0;
+    return hla::kStatusBytes + hla::delta::backward_bytes(sizes(dtype, B, Hk, H, T, d, dv));
+}
+
+int hla_delta_backward_kernel_launches(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
+    if (check_shape(dtype, B, Hk, H, T, d, dv) != HLA_OK) return 0;
+    return hla::delta::backward_launches(sizes(dtype, B, Hk, H, T, d, dv));
+}
+
+hla_status_t hla_delta_backward(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                const float* state_in, const int* lengths, const void* dout,
+                                const float* dstate_out, void* dq, void* dk, void* dv_out, float* dg, float* dbeta,
+                                float* dstate_in, int B, int Hk, int H, int T, int d, int dv, hla_dtype_t dtype,
+                                hla_layout_t layout, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv_out || !dg || !dbeta) return HLA_ERR_NULL;
+    const hla_status_t s = check_shape(dtype, B, Hk, H, T, d, dv);
+    if (s != HLA_OK) return s;
+    if (layout != HLA_BHTD && layout != HLA_BTHD) return HLA_ERR_UNSUPPORTED;
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(dout, 16) ||
+        misaligned(state_in, 16) || misaligned(dstate_out, 16) || misaligned(dq, 16) || misaligned(dk, 16) ||
+        misaligned(dv_out, 16) || misaligned(dstate_in, 16) || misaligned(g, 4) || misaligned(beta, 4) ||
+        misaligned(dg, 4) || misaligned(dbeta, 4) || misaligned(lengths, 4))
+        return HLA_ERR_ALIGN;
+    if (!workspace) return HLA_ERR_WORKSPACE;
+    if (misaligned(workspace, 16)) return HLA_ERR_ALIGN;
+    if (workspace_bytes < hla_delta_backward_workspace_bytes(dtype, B, Hk, H, T, d, dv)) return HLA_ERR_WORKSPACE;
+    hla::delta::Problem p = sizes(dtype, B, Hk, H, T, d, dv);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.state_in = state_in; p.lengths = lengths;
+    p.bthd = layout == HLA_BTHD;
+    p.scale = scale;
+    const hla::delta::Gradients gr{dout, dstate_out, dq, dk, dv_out, dg, dbeta, dstate_in};
+    void* body = static_cast<char*>(workspace) + hla::kStatusBytes;
+    return hla::delta::backward(p, gr, body, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
 
 hla_status_t hla_group_norm_forward(const void* x, const void* gate, const float* weight, const float* bias,

@@ -1,0 +1,812 @@
+// Gradients of the gated delta rule.
+//
+// With a chunk's terms as in delta_forward.cu, dS the gradient at the state behind the chunk, and
+//     dU = P^T dO + diag(e^(c_C - c)) K dS
+//     H  = ((I + diag(beta) M)^-1)^T dU        (the gradient at U with all that U feeds)
+//     Z  = diag(beta) H                        (the gradient at R, and at V)
+// the gradient at the state before the chunk is
+//     dS0 = e^(c_C) dS + (scale e^c Q)^T dO - (e^c K)^T Z.
+// Three passes: the forward walk again, which keeps the states before blocks of chunks and R; this
+// reverse walk, which keeps dS behind the blocks and H; and one kernel over all blocks, which has
+// then everything for dq, dk, dv, dbeta and dg.  R and H are per token, not per chunk (R is a token's
+// error, H the gradient at what it writes), so the blocks need not be the walks' chunks.
+#include <type_traits>
+
+#include "delta_walk.cuh"
+
+namespace hla {
+namespace delta {
+namespace {
+
+// ------------------------------------------------------------------ reverse walk
+struct ReverseArgs {
+    const void *q, *k, *dout;
+    const uint8_t* records;   // gradients' form
+    const float* dstate_out;  // [BH][d][dv] or null
+    const int* lengths;
+    float* dstate_in;         // [BH][d][dv] or null
+    float* dstates;           // [BH][blocks][d][dv]: dS behind each block
+    float* H;                 // [BH][T][dv]
+    int Hk, Hv, T, dv, bthd, block_chunks;
+    float scale;
+};
+
+template <typename E, int DK_, int NG_>
+struct Rev {
+    using Elem = E;
+    static constexpr int DK = DK_, CS = 16 * NG_;
+    static constexpr bool BF = sizeof(E) == 2;
+    static constexpr int KT = BF ? 1 : 3;
+    static constexpr int AHEAD = BF ? 3 : 1, NS = AHEAD + 1, NLD = BF ? 2 : 4;
+    static constexpr int NH = DK_ == 128 ? 4 : 2, W_STATE = NH * NG_, WARPS = W_STATE + NLD;
+    static constexpr int KTILE = KT * C * DK_ * 2, OTILE = KT * C * CS * 2, PB = 3 * C * C * 2;
+    // a stage
+    static constexpr int k = 0, q = k + KTILE, x = q + KTILE, p = x + kXBytes, dO = p + PB, gates = dO + OTILE;
+    static constexpr int STAGE = (gates + 512 + 255) / 256 * 256;
+    static constexpr int ex = NS * STAGE;               // partial sums, then the decayed Z
+    static constexpr int YB = 2 * 3 * 512;
+    static constexpr int yf = ex + W_STATE * 2048;      // dU as an A operand
+    static constexpr int wf = yf + NG_ * YB;            // scale e^c dO as an A operand
+    static constexpr int bytes = wf + NG_ * YB;
+};
+
+template <typename F>
+__global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const ReverseArgs a) {
+    using E = typename F::Elem;
+    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, CS = F::CS, KT = F::KT;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = ptx::smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slices = a.dv / CS, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * CS;
+    const int b = bh / a.Hv, h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int T = length_of(a.lengths, b, a.T);
+    const int all_chunks = (a.T + C - 1) / C, chunks = (T + C - 1) / C;
+    const int blocks = (all_chunks + a.block_chunks - 1) / a.block_chunks;
+    const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.Hv);
+    constexpr int w_load = F::W_STATE;
+    const int grp = warp / NH, part = warp % NH;
+
+    float S[DH / 8][4];                                 // dS^T, as the forward walk holds S^T
+    const int own_col = col0 + 16 * grp + (lane >> 2), own_key = part * DH + 2 * (lane & 3);
+    if (warp < w_load) {
+        const float* from = a.dstate_out ? a.dstate_out + static_cast<long long>(bh) * DK * a.dv : nullptr;
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                S[n][j] = from ? from[static_cast<long long>(own_key + 8 * n + (j & 1)) * a.dv + own_col + 8 * (j >> 1)] : 0.f;
+    }
+    constexpr int ALL = F::WARPS * 32;
+    const auto step_end = [] { ptx::named_sync(15, ALL); };
+    if (chunks > 0 && warp < w_load) {
+        const uint32_t k_n = at_pieces_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
+        const uint32_t k_t = at_rows_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
+        const uint32_t q_t = at_rows_first<DK * 2>(sb + F::q, 0, part * (DH / 8), lane);
+        float4* const ex = reinterpret_cast<float4*>(sm + F::ex) + grp * NH * 128 + lane;
+        uint8_t* const yf = sm + F::yf + grp * F::YB;
+        uint8_t* const wf = sm + F::wf + grp * F::YB;
+        uint8_t* const vf = reinterpret_cast<uint8_t*>(ex - lane);
+        int stage = 0;
+        for (int s = -F::AHEAD; s < 0; ++s) step_end();
+        for (int c = chunks - 1; c >= 0; --c) {
+            const uint32_t so = stage * F::STAGE;
+            const Gates* G = reinterpret_cast<const Gates*>(sm + stage * F::STAGE + F::gates);
+            if (c % a.block_chunks == a.block_chunks - 1 || c == chunks - 1) {
+                float* to = a.dstates + (static_cast<long long>(bh) * blocks + c / a.block_chunks) * DK * a.dv +
+                            static_cast<long long>(own_key) * a.dv + own_col;
+#pragma unroll
+                for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) to[static_cast<long long>(8 * n + (j & 1)) * a.dv + 8 * (j >> 1)] = S[n][j];
+            }
+            // this part's share of dS^T K^T, all tokens
+            float y[4][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks) {
+                uint32_t bk[2][KT][4];
+#pragma unroll
+                for (int np = 0; np < 2; ++np)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+                        ldsm4(bk[np][t], ((k_n + so) ^ (ks << 5)) + t * (C * DK * 2) + np * 16 * DK * 2);
+                uint32_t as[3][4];
+                split_a<3>(S[2 * ks], S[2 * ks + 1], as);
+                prod<3, KT, 2>(y, as, bk);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (n / TN != part) ex[(part * 4 + n) * 32] = make_float4(y[n][0], y[n][1], y[n][2], y[n][3]);
+            // meanwhile, for the tokens of this part: dO^T P, and scale e^c dO^T for the state
+            float2 since[TN], beta[TN], left[TN];
+            float z[TN][4];
+            uint32_t ao[2][KT][4];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int t = 0; t < KT; ++t)      // [col][token] out of rows of tokens: transposed 8 x 8 blocks
+                    ldsm4t(ao[kk][t], sb + F::dO + so + t * (C * CS * 2) +
+                                          piece<CS * 2>(16 * kk + (lane >> 4) * 8 + (lane & 7), 2 * grp + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e, tok = 8 * n + 2 * (lane & 3);
+                since[e] = *reinterpret_cast<const float2*>(&G->since[tok]);
+                beta[e] = *reinterpret_cast<const float2*>(&G->beta[tok]);
+                left[e] = *reinterpret_cast<const float2*>(&G->left[tok]);
+                uint32_t bp[3][4];
+#pragma unroll
+                for (int t = 0; t < 3; ++t)       // P[i][j], i the summed axis: all four blocks of rows of piece n
+                    ldsm4t(bp[t], sb + F::p + so + t * (C * C * 2) + piece<C * 2>(lane, n));
+                float r[2][4] = {};
+                constexpr int M = 3;
+#pragma unroll
+                for (int i = 0; i < KT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (i + j < M) {
+                            mma16816(r[1], ao[1][i], bp[j][2], bp[j][3]);
+                            if (n < 2) mma16816(r[0], ao[0][i], bp[j][0], bp[j][1]);
+                        }
+                // the outputs' gradients of this tile themselves, in the accumulators' layout
+                float o[4] = {};
+#pragma unroll
+                for (int t = KT - 1; t >= 0; --t) {
+                    // registers 0, 1: the first tile of 16 tokens, 2, 3: the second (constant indexes only)
+                    const uint32_t lo = n < 2 ? ((n & 1) ? ao[0][t][2] : ao[0][t][0]) : ((n & 1) ? ao[1][t][2] : ao[1][t][0]);
+                    const uint32_t hi = n < 2 ? ((n & 1) ? ao[0][t][3] : ao[0][t][1]) : ((n & 1) ? ao[1][t][3] : ao[1][t][1]);
+                    o[0] += __uint_as_float(lo << 16); o[1] += __uint_as_float(lo & 0xffff0000u);
+                    o[2] += __uint_as_float(hi << 16); o[3] += __uint_as_float(hi & 0xffff0000u);
+                }
+                uint32_t t0[3], t1[3];
+                const float f0 = a.scale * since[e].x, f1 = a.scale * since[e].y;
+                split<3>(o[0] * f0, o[1] * f1, t0);
+                split<3>(o[2] * f0, o[3] * f1, t1);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    reinterpret_cast<uint2*>(wf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[e][j] = r[0][j] + r[1][j];
+            }
+            uint32_t bx[TN][3][4];
+#pragma unroll
+            for (int e = 0; e < TN; ++e)
+#pragma unroll
+                for (int t = 0; t < 3; ++t)       // X'[j][i], j the summed axis
+                    ldsm4t(bx[e][t], sb + F::x + so + t * (C * C * 2) + piece<C * 2>(lane, part * TN + e));
+            float mine[TN][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (n / TN == part)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mine[n % TN][j] = y[n][j];
+            ptx::named_sync(1 + grp, NH * 32);
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e;
+                float w[4] = {mine[e][0], mine[e][1], mine[e][2], mine[e][3]};
+#pragma unroll
+                for (int o = 1; o < NH; ++o) {
+                    const float4 x = ex[((part ^ o) * 4 + n) * 32];
+                    w[0] += x.x; w[1] += x.y; w[2] += x.z; w[3] += x.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[e][j] = fmaf((j & 1) ? left[e].y : left[e].x, w[j], z[e][j]);
+                uint32_t t0[3], t1[3];
+                split<3>(z[e][0], z[e][1], t0);
+                split<3>(z[e][2], z[e][3], t1);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    reinterpret_cast<uint2*>(yf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
+            }
+            const float all = G->all;
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[n][j] *= all;
+            ptx::named_sync(1 + grp, NH * 32);
+            // scale (e^c Q)^T dO, transposed: all parts have shared theirs by now
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t au[3][4], bq[DH / 16][KT][4];
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint4 u = reinterpret_cast<const uint4*>(wf)[(kk * 3 + t) * 32 + lane];
+                    au[t][0] = u.x; au[t][1] = u.y; au[t][2] = u.z; au[t][3] = u.w;
+                }
+#pragma unroll
+                for (int np = 0; np < DH / 16; ++np)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+                        ldsm4t(bq[np][t], ((q_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                prod<3, KT, DH / 16>(S, au, bq);
+            }
+            // H^T = dU^T X' for the tokens of this part; X'[j][i] is zero above the diagonal (j < i)
+            uint32_t ay[2][3][4];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint4 u = reinterpret_cast<const uint4*>(yf)[(kk * 3 + t) * 32 + lane];
+                    ay[kk][t][0] = u.x; ay[kk][t][1] = u.y; ay[kk][t][2] = u.z; ay[kk][t][3] = u.w;
+                }
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e;
+                float r[4][4] = {};
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3 - i; ++j) {
+                        mma16816(r[2 + ((i + j) & 1)], ay[1][i], bx[e][j][2], bx[e][j][3]);
+                        if (n < 2) mma16816(r[(i + j) & 1], ay[0][i], bx[e][j][0], bx[e][j][1]);
+                    }
+                float u[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] = (r[0][j] + r[1][j]) + (r[2][j] + r[3][j]);
+                const int tok = c * C + 8 * n + 2 * (lane & 3);
+                float* to = a.H + (static_cast<long long>(bh) * a.T + tok) * a.dv + own_col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (tok + (j & 1) < T) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[j];
+                const float f0 = -since[e].x * beta[e].x, f1 = -since[e].y * beta[e].y;
+                uint32_t t0[3], t1[3];
+                split<3>(u[0] * f0, u[1] * f1, t0);
+                split<3>(u[2] * f0, u[3] * f1, t1);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    reinterpret_cast<uint2*>(vf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
+            }
+            ptx::named_sync(1 + grp, NH * 32);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t au[3][4], bt[DH / 16][KT][4];
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint4 u = reinterpret_cast<const uint4*>(vf)[(kk * 3 + t) * 32 + lane];
+                    au[t][0] = u.x; au[t][1] = u.y; au[t][2] = u.z; au[t][3] = u.w;
+                }
+#pragma unroll
+                for (int np = 0; np < DH / 16; ++np)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+                        ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                prod<3, KT, DH / 16>(S, au, bt);
+            }
+            if (++stage == F::NS) stage = 0;
+            step_end();
+        }
+    } else if (chunks > 0) {
+        const int lt = (warp - w_load) * 32 + lane;
+        constexpr int LT = F::NLD * 32, REC = record_bytes(2, 3);
+        const long long ks = static_cast<long long>(kstep) * DK, vs = static_cast<long long>(vstep) * a.dv;
+        const E* kp = static_cast<const E*>(a.k) + row_of(a.bthd, b, hk, a.Hk, 0, a.T) * DK;
+        const E* qp = static_cast<const E*>(a.q) + row_of(a.bthd, b, hk, a.Hk, 0, a.T) * DK;
+        const E* op = static_cast<const E*>(a.dout) + row_of(a.bthd, b, h, a.Hv, 0, a.T) * a.dv + col0;
+        const uint8_t* rec = a.records + static_cast<long long>(bh) * all_chunks * REC;
+        int stage = 0;
+        for (int i = 0; i < chunks + F::AHEAD; ++i) {
+            const int c = chunks - 1 - i;
+            if (c >= 0) {
+                const uint32_t sg = sb + stage * F::STAGE;
+                const int rows = min(C, T - c * C);
+                const uint8_t* from = rec + static_cast<long long>(c) * REC + kXBytes;
+                load_bytes<kXBytes + F::PB, LT>(sg + F::x, from, lt);      // X' and P lie one behind the other
+                load_bytes<512, LT>(sg + F::gates, from + kXBytes + F::PB, lt);
+                load_tile<CS, KT, LT>(sg + F::dO, op + static_cast<long long>(c) * C * vs, vs, rows, lt);
+                load_tile<DK, KT, LT>(sg + F::k, kp + static_cast<long long>(c) * C * ks, ks, rows, lt);
+                load_tile<DK, KT, LT>(sg + F::q, qp + static_cast<long long>(c) * C * ks, ks, rows, lt);
+                if (++stage == F::NS) stage = 0;
+            }
+            cp_commit();
+            cp_wait<F::AHEAD - 1>();
+            step_end();
+        }
+    }
+    if (warp < w_load && a.dstate_in) {
+        float* to = a.dstate_in + static_cast<long long>(bh) * DK * a.dv;
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                to[static_cast<long long>(own_key + 8 * n + (j & 1)) * a.dv + own_col + 8 * (j >> 1)] = S[n][j];
+    }
+}
+
+// ------------------------------------------------------------------ gradients of a block
+// A block of N tokens (c, D, e^c from the block's first token), S0 before it, dS behind it, a warp
+// to 16 tokens:
+//     dq  = scale e^c dO S0^T + (scale D dO U^T) K
+//     dk  = -e^c Z S0^T + (-D Z U^T) K                                  (as a row of M)
+//         + e^(c_N - c) U dS^T + (scale D dO U^T)^T Q + (-D Z U^T)^T K    (as a column)
+// and the gradient at c, of which every term is a product already taken:
+//     dc_i = q_i . dq_i + k_i . dk_i(row) - k_i . dk_i(column),  dc_N += <dS, S behind the block>
+struct BlockArgs {
+    const void *q, *k, *dout;
+    const float *g, *beta, *states, *dstates, *R, *H;
+    const int* lengths;
+    void *dq, *dk, *dv;       // dq, dk: gradients, or with shared heads fp32 [BH][T][d] (PARTIAL)
+    float *dg, *dbeta;
+    int B, Hk, Hv, T, blocks, bthd;
+    float scale;
+};
+
+template <typename E, int DK_, int DV_, int N_>
+struct Blk {
+    using Elem = E;
+    static constexpr int DK = DK_, DV = DV_, N = N_, WARPS = N_ / 16, NT = WARPS * 32;
+    static constexpr int KT = sizeof(E) == 2 ? 1 : 3;
+    static constexpr int SW = DV_ < 32 ? DV_ : 32;      // value columns of a state at a time
+    static constexpr int KTERM = N * DK * 2, OTERM = N * DV * 2, STERM = DK * SW * 2;
+    static constexpr int k = 0, q = k + KT * KTERM, o = q + KT * KTERM, u = o + KT * OTERM, z = u + 3 * OTERM;
+    static constexpr int s = z + 3 * OTERM;
+    static constexpr int sum = s + 3 * STERM, since = sum + N * 8, left = since + N * 4, beta = left + N * 4;
+    static constexpr int dc = beta + N * 4, red = dc + N * 4;
+    static constexpr int bytes = red + 64 * 4;
+};
+
+// R rows x D columns of fp32 (times fac[row] where given) into three swizzled bf16 terms.
+template <int RB, int R, int D, int NT>
+__device__ __forceinline__ void load_split(uint32_t tile, uint32_t term, const float* src, long long step, int rows, int tid,
+                                           const float* fac) {
+    constexpr int P = D / 4, U = 4;
+#pragma unroll 1
+    for (int i0 = tid; i0 < R * P; i0 += NT * U) {
+        float4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * NT, r = i / P, c = i % P;
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < R * P && r < rows) x[u] = *reinterpret_cast<const float4*>(src + r * step + c * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * NT, r = i / P, c = i % P;
+            if (i >= R * P) continue;
+            const float w = fac ? fac[r] : 1.f;
+            uint32_t lo[3], hi[3];
+            split<3>(x[u].x * w, x[u].y * w, lo);
+            split<3>(x[u].z * w, x[u].w * w, hi);
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tile + t * term + piece<RB>(r, c >> 1) + (c & 1) * 8),
+                             "r"(lo[t]), "r"(hi[t]) : "memory");
+        }
+    }
+}
+
+// N rows of E into KT swizzled terms.
+template <int N, int D, int KT, int NT>
+__device__ __forceinline__ void load_rows(uint32_t tile, const bf16* src, long long step, int rows, int tid) {
+    constexpr int P = D / 8;
+#pragma unroll 4
+    for (int i = tid; i < N * P; i += NT) {
+        const int r = i / P, c = i % P;
+        const bool on = r < rows;
+        cp_async16(tile + piece<D * 2>(r, c), src + (on ? r * step : 0) + c * 8, on);
+    }
+}
+template <int N, int D, int KT, int NT>
+__device__ __forceinline__ void load_rows(uint32_t tile, const float* src, long long step, int rows, int tid) {
+    load_split<D * 2, N, D, NT>(tile, N * D * 2, src, step, rows, tid, nullptr);
+}
+
+// sum over this lane's columns of acc[row] * tile[row], rows r0 + lane / 4 (+ 8); all four lanes get it
+template <int D, int KT>
+__device__ __forceinline__ void row_dots(const float (&acc)[D / 8][4], const uint8_t* tile, int term, int r0, int lane,
+                                         float (&out)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = r0 + (lane >> 2) + 8 * h;
+        float s = 0.f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int t = KT - 1; t >= 0; --t) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + t * term + piece<D * 2>(r, n) + (lane & 3) * 4);
+                x0 += __uint_as_float(w << 16);
+                x1 += __uint_as_float(w & 0xffff0000u);
+            }
+            s = fmaf(acc[n][2 * h], x0, s);
+            s = fmaf(acc[n][2 * h + 1], x1, s);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        out[h] = s + __shfl_xor_sync(0xffffffffu, s, 2);
+    }
+}
+
+// acc[16 tokens][DK] += rows of `at` (AT terms) x state^T, the state in slices of SW columns (the
+// whole block takes part).
+template <typename F, int AT>
+__device__ __forceinline__ void with_state(float (&acc)[F::DK / 8][4], uint32_t sb, int at, const float* state, int tid) {
+    constexpr int DK = F::DK, DV = F::DV, SW = F::SW;
+    const int lane = tid & 31, r0 = (tid >> 5) * 16;
+#pragma unroll 1
+    for (int c0 = 0; c0 < DV; c0 += SW) {
+        __syncthreads();
+        load_split<SW * 2, DK, SW, F::NT>(sb + F::s, F::STERM, state + c0, DV, DK, tid, nullptr);
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < SW / 16; ++ks) {
+            uint32_t x[AT][4];
+#pragma unroll
+            for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
+#pragma unroll
+            for (int np = 0; np < DK / 16; ++np) {
+                uint32_t y[3][4];
+#pragma unroll
+                for (int t = 0; t < 3; ++t) ldsm4(y[t], at_pieces_first<SW * 2>(sb + F::s + t * F::STERM, 16 * np, 2 * ks, lane));
+                prod2<AT, 3>(acc[2 * np], acc[2 * np + 1], x, y);
+            }
+        }
+    }
+}
+
+// acc += (f D o (X Y^T)) B over the 16 x 16 blocks of one side of the diagonal: X the rows of this
+// warp's tokens, Y and B rows of the whole block.  ROWS: this warp's tokens are i (D_ij counts for
+// j <= i, for j < i when STRICT), else they are j.
+template <typename F, int AT, int YT, bool ROWS, bool STRICT>
+__device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t sb, const float2* sum, int at, int yt, int bt,
+                                           float f, int tid) {
+    constexpr int DK = F::DK, DV = F::DV, KT = F::KT;
+    const int lane = tid & 31, warp = tid >> 5, r0 = warp * 16;
+#pragma unroll 1
+    for (int jb = ROWS ? 0 : warp; jb <= (ROWS ? warp : F::WARPS - 1); ++jb) {
+        float w[2][4] = {};
+#pragma unroll 2
+        for (int ks = 0; ks < DV / 16; ++ks) {
+            uint32_t x[AT][4], y[YT][4];
+#pragma unroll
+            for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, 2 * ks, lane));
+#pragma unroll
+            for (int t = 0; t < YT; ++t) ldsm4(y[t], at_pieces_first<DV * 2>(sb + yt + t * F::OTERM, 16 * jb, 2 * ks, lane));
+            prod2<AT, YT>(w[0], w[1], x, y);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int mine = r0 + (lane >> 2) + 8 * (j >> 1), other = 16 * jb + 8 * n + 2 * (lane & 3) + (j & 1);
+                const int i = ROWS ? mine : other, k = ROWS ? other : mine;
+                const float2 x = sum[i], y = sum[k];
+                w[n][j] = (STRICT ? k < i : k <= i) ? f * w[n][j] * ex2((x.x - y.x) + (x.y - y.y)) : 0.f;
+            }
+        uint32_t x[3][4];
+        split_a<3>(w[0], w[1], x);
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np) {
+            uint32_t y[KT][4];
+#pragma unroll
+            for (int t = 0; t < KT; ++t) ldsm4t(y[t], at_rows_first<DK * 2>(sb + bt + t * F::KTERM, 16 * jb, 2 * np, lane));
+            prod2<3, KT>(acc[2 * np], acc[2 * np + 1], x, y);
+        }
+    }
+}
+
+template <int NT_>
+__device__ __forceinline__ void clear(float (&acc)[NT_][4]) {
+#pragma unroll
+    for (int n = 0; n < NT_; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+}
+// acc[row] *= f of[row], rows r0 + lane / 4 (+ 8)
+template <int NT_>
+__device__ __forceinline__ void by_row(float (&acc)[NT_][4], const float* of, float f, int r0, int lane) {
+    const float x = f * of[r0 + (lane >> 2)], y = f * of[r0 + 8 + (lane >> 2)];
+#pragma unroll
+    for (int n = 0; n < NT_; ++n) {
+        acc[n][0] *= x; acc[n][1] *= x; acc[n][2] *= y; acc[n][3] *= y;
+    }
+}
+// rows r0 + lane / 4 (+ 8) of acc to rows of `to` (`step` elements apart); zeros from `rows` on
+template <typename O, int NT_>
+__device__ __forceinline__ void write_rows(const float (&acc)[NT_][4], O* to, long long step, int r0, int rows, int out_rows, int lane) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + (lane >> 2) + 8 * e;
+        if (r >= out_rows) continue;
+#pragma unroll
+        for (int n = 0; n < NT_; ++n) {
+            const float x0 = r < rows ? acc[n][2 * e] : 0.f, x1 = r < rows ? acc[n][2 * e + 1] : 0.f;
+            O* at = to + r * step + 8 * n + 2 * (lane & 3);
+            if constexpr (sizeof(O) == 2) *reinterpret_cast<uint32_t*>(at) = ptx::pack_bf16(x0, x1);
+            else *reinterpret_cast<float2*>(at) = make_float2(x0, x1);
+        }
+    }
+}
+
+template <typename F, bool PARTIAL>
+__global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) {
+    using E = typename F::Elem;
+    constexpr int DK = F::DK, DV = F::DV, N = F::N, KT = F::KT, NT = F::NT, SW = F::SW;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = ptx::smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = 16 * warp;
+    const int bh = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
+    const int b = bh / a.Hv, h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int t0 = blk * N, T = length_of(a.lengths, b, a.T);
+    const int rows = max(0, min(N, T - t0)), out_rows = min(N, a.T - t0);
+    const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.Hv);
+    const long long kr = row_of(a.bthd, b, hk, a.Hk, t0, a.T), vr = row_of(a.bthd, b, h, a.Hv, t0, a.T);
+    float2* sum = reinterpret_cast<float2*>(sm + F::sum);
+    float* since = reinterpret_cast<float*>(sm + F::since);
+    float* left = reinterpret_cast<float*>(sm + F::left);
+    float* beta = reinterpret_cast<float*>(sm + F::beta);
+    float* dc = reinterpret_cast<float*>(sm + F::dc);
+    float* red = reinterpret_cast<float*>(sm + F::red);
+    const float* R = a.R + (static_cast<long long>(bh) * a.T + t0) * DV;
+    const float* H = a.H + (static_cast<long long>(bh) * a.T + t0) * DV;
+    const float* S0 = a.states + (static_cast<long long>(bh) * a.blocks + blk) * DK * DV;
+    const float* dS = a.dstates + (static_cast<long long>(bh) * a.blocks + blk) * DK * DV;
+
+    if (rows > 0) {
+        load_rows<N, DK, KT, NT>(sb + F::k, static_cast<const E*>(a.k) + kr * DK, static_cast<long long>(kstep) * DK, rows, tid);
+        load_rows<N, DK, KT, NT>(sb + F::q, static_cast<const E*>(a.q) + kr * DK, static_cast<long long>(kstep) * DK, rows, tid);
+        load_rows<N, DV, KT, NT>(sb + F::o, static_cast<const E*>(a.dout) + vr * DV, static_cast<long long>(vstep) * DV, rows, tid);
+        cp_commit();
+    }
+    if (warp == 0) {
+        double c = 0.0, last = 0.0, keep[N / 32];
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+            const int r = 32 * i + lane;
+            const bool on = r < rows;
+            beta[r] = on ? a.beta[vr + static_cast<long long>(r) * vstep] : 0.f;
+            c = on ? static_cast<double>(gate(a.g[vr + static_cast<long long>(r) * vstep])) * 1.4426950408889634 : 0.0;
+#pragma unroll
+            for (int w = 1; w < 32; w <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, c, w);
+                if (lane >= w) c += x;
+            }
+            c += last;
+            last = __shfl_sync(0xffffffffu, c, 31);
+            keep[i] = c;
+        }
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+            const int r = 32 * i + lane;
+            const float hi = static_cast<float>(keep[i]);
+            sum[r] = make_float2(hi, static_cast<float>(keep[i] - static_cast<double>(hi)));
+            since[r] = ex2_long(keep[i]);
+            left[r] = ex2_long(last - keep[i]);
+        }
+    }
+    __syncthreads();
+    // dv = Z and dbeta = R . H, a row a warp at a time; then U and Z for the products
+    for (int r = warp; r < out_rows; r += F::WARPS) {
+        const bool on = r < rows;
+        const float bt = beta[r];
+        E* dv = static_cast<E*>(a.dv) + (vr + static_cast<long long>(r) * vstep) * DV;
+        float s = 0.f;
+#pragma unroll
+        for (int c = lane; c < DV; c += 32) {
+            const float x = on ? H[static_cast<long long>(r) * DV + c] : 0.f, y = on ? R[static_cast<long long>(r) * DV + c] : 0.f;
+            s = fmaf(x, y, s);
+            store_elem(dv + c, on ? bt * x : 0.f);
+        }
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        if (lane == 0) a.dbeta[vr + static_cast<long long>(r) * vstep] = s;
+    }
+    if (rows <= 0) {
+        for (int i = tid; i < out_rows * DK; i += NT) {
+            const int r = i / DK, c = i % DK;
+            if (PARTIAL) {
+                const long long at = (static_cast<long long>(bh) * a.T + t0 + r) * DK + c;
+                static_cast<float*>(a.dq)[at] = 0.f;
+                static_cast<float*>(a.dk)[at] = 0.f;
+            } else {
+                const long long at = (kr + static_cast<long long>(r) * kstep) * DK + c;
+                store_elem(static_cast<E*>(a.dq) + at, 0.f);
+                store_elem(static_cast<E*>(a.dk) + at, 0.f);
+            }
+        }
+        for (int r = tid; r < out_rows; r += NT) a.dg[vr + static_cast<long long>(r) * vstep] = 0.f;
+        return;
+    }
+    load_split<DV * 2, N, DV, NT>(sb + F::u, F::OTERM, R, DV, rows, tid, beta);
+    load_split<DV * 2, N, DV, NT>(sb + F::z, F::OTERM, H, DV, rows, tid, beta);
+    // <dS, S0>
+    float cross = 0.f;
+#pragma unroll 4
+    for (int i = tid * 4; i < DK * DV; i += NT * 4) {
+        float x[4], y[4];
+        load4(S0 + i, x);
+        load4(dS + i, y);
+        cross += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, w);
+    if (lane == 0) red[warp] = cross;
+    cp_wait<0>();
+    __syncthreads();
+
+    // where dq and dk go: the gradients, or this value head's share of them
+    using O = std::conditional_t<PARTIAL, float, E>;
+    const long long out_at = (PARTIAL ? static_cast<long long>(bh) * a.T + t0 : kr) * DK;
+    const long long out_step = static_cast<long long>(PARTIAL ? 1 : kstep) * DK;
+    O* const dq = static_cast<O*>(a.dq) + out_at;
+    O* const dk = static_cast<O*>(a.dk) + out_at;
+    float acc[DK / 8][4], row_dk[DK / 8][4];
+    float dcs[2], d1[2], d2[2], d3[2];
+    clear(acc);
+    with_state<F, KT>(acc, sb, F::o, S0, tid);
+    by_row(acc, since, a.scale, r0, lane);
+    with_pairs<F, KT, 3, true, false>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid);
+    write_rows(acc, dq, out_step, r0, rows, out_rows, lane);
+    row_dots<DK, KT>(acc, sm + F::q, F::KTERM, r0, lane, dcs);
+    clear(row_dk);
+    with_state<F, 3>(row_dk, sb, F::z, S0, tid);
+    by_row(row_dk, since, -1.f, r0, lane);
+    with_pairs<F, 3, 3, true, true>(row_dk, sb, sum, F::z, F::u, F::k, -1.f, tid);
+    row_dots<DK, KT>(row_dk, sm + F::k, F::KTERM, r0, lane, d1);       // k . dk(row)
+    // the column terms on their own: they leave dc with the other sign
+    clear(acc);
+    with_state<F, 3>(acc, sb, F::u, dS, tid);
+    by_row(acc, left, 1.f, r0, lane);
+    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, d2);          // the writes' part of <dS, S>
+    with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, tid);
+    with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, tid);
+    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, d3);          // k . dk(column)
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][j] += row_dk[n][j];
+    write_rows(acc, dk, out_step, r0, rows, out_rows, lane);
+    if ((lane & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) dc[r0 + (lane >> 2) + 8 * e] = dcs[e] + d1[e] - d3[e];
+    }
+    float end = (lane & 3) == 0 ? d2[0] + d2[1] : 0.f;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) end += __shfl_xor_sync(0xffffffffu, end, w);
+    if (lane == 0) red[32 + warp] = end;
+    __syncthreads();
+    if (warp == 0) {
+        // dg_i = sum of dc from i on; the state behind the block counts as one more term at its end
+        float tail = 0.f, cr = 0.f;
+#pragma unroll
+        for (int i = 0; i < F::WARPS; ++i) {
+            cr += red[i];
+            tail += red[32 + i];
+        }
+        tail = fmaf(since[N - 1], cr, tail);
+#pragma unroll
+        for (int i = N / 32 - 1; i >= 0; --i) {
+            const int r = 32 * i + lane;
+            float x = dc[r];
+#pragma unroll
+            for (int w = 1; w < 32; w <<= 1) {
+                const float y = __shfl_down_sync(0xffffffffu, x, w);
+                if (lane + w < 32) x += y;
+            }
+            x += tail;
+            tail = __shfl_sync(0xffffffffu, x, 0);
+            if (r < out_rows) a.dg[vr + static_cast<long long>(r) * vstep] = r < rows ? x : 0.f;
+        }
+    }
+}
+
+// Shared heads: dq, dk of a key head are the sums over its value heads, in their order.
+template <typename E>
+__global__ void __launch_bounds__(256) k_delta_share(const float* dq, const float* dk, E* oq, E* ok, int B, int Hk, int share,
+                                                     int T, int d, int bthd) {
+    const long long per = static_cast<long long>(T) * d / 4, n = static_cast<long long>(B) * Hk * per;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * 256) {
+        const long long bhk = i / per, at = (i % per) * 4;
+        const int b = static_cast<int>(bhk / Hk), hk = static_cast<int>(bhk % Hk);
+        const int t = static_cast<int>(at / d), c = static_cast<int>(at % d);
+        float x[4] = {}, y[4] = {};
+        for (int s = 0; s < share; ++s) {
+            const long long from = ((static_cast<long long>(b) * Hk + hk) * share + s) * T * d + at;
+            float u[4], w[4];
+            load4(dq + from, u);
+            load4(dk + from, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] += u[j], y[j] += w[j];
+        }
+        const long long to = row_of(bthd, b, hk, Hk, t, T) * d + c;
+        store4(oq + to, x);
+        store4(ok + to, y);
+    }
+}
+
+// ------------------------------------------------------------------ host
+// Tokens of a block: 64, or 32 where the fp32 tiles of 64 do not fit.
+int block_tokens(const Problem& p) { return !p.bf16 && (p.d == 128 || p.dv == 128) ? 32 : 64; }
+
+struct Space {   // the workspace's pieces, bytes from its start
+    size_t records, states, dstates, R, H, dq, dk, end;
+};
+Space space(const Problem& p) {
+    const size_t BH = static_cast<size_t>(p.B) * p.H, blocks = (p.T + block_tokens(p) - 1) / block_tokens(p);
+    const size_t state = BH * blocks * p.d * p.dv * 4, rows = BH * p.T * p.dv * 4;
+    const size_t part = p.H != p.Hk ? BH * p.T * p.d * 4 : 0;
+    Space s;
+    s.records = 0;
+    s.states = s.records + records_bytes(p, true);
+    s.dstates = s.states + state;
+    s.R = s.dstates + state;
+    s.H = s.R + rows;
+    s.dq = s.H + rows;
+    s.dk = s.dq + part;
+    s.end = s.dk + part;
+    return s;
+}
+
+template <typename E, int DK>
+cudaError_t reverse(const Problem& p, const Gradients& gr, const uint8_t* records, float* dstates, float* H, cudaStream_t st) {
+    using F = Rev<E, DK, sizeof(E) == 2 ? 2 : 1>;
+    static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
+    const ReverseArgs a{p.q, p.k, gr.dout, records, gr.dstate_out, p.lengths, gr.dstate_in, dstates, H,
+                        p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, block_tokens(p) / C, p.scale};
+    cudaError_t e = cudaFuncSetAttribute(k_delta_reverse<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    if (e != cudaSuccess) return e;
+    k_delta_reverse<F><<<p.B * p.H * (p.dv / F::CS), F::WARPS * 32, F::bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, int DK, int DV>
+cudaError_t block_grads(const Problem& p, const Gradients& gr, char* ws, const Space& s, cudaStream_t st) {
+    constexpr int N = sizeof(E) == 4 && (DK == 128 || DV == 128) ? 32 : 64;
+    using F = Blk<E, DK, DV, N>;
+    static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
+    const bool shared = p.H != p.Hk;
+    const int blocks = (p.T + N - 1) / N;
+    const BlockArgs a{p.q, p.k, gr.dout, p.g, p.beta, reinterpret_cast<float*>(ws + s.states),
+                      reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.R),
+                      reinterpret_cast<float*>(ws + s.H), p.lengths, shared ? ws + s.dq : gr.dq, shared ? ws + s.dk : gr.dk,
+                      gr.dv, gr.dg, gr.dbeta, p.B, p.Hk, p.H, p.T, blocks, p.bthd ? 1 : 0, p.scale};
+    void (*kernel)(const BlockArgs) = k_delta_block_grads<F, false>;
+    if (shared) kernel = k_delta_block_grads<F, true>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<p.B * p.H * blocks, F::NT, F::bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E, int DK>
+cudaError_t all(const Problem& p, const Gradients& gr, char* ws, cudaStream_t st) {
+    const Space s = space(p);
+    uint8_t* records = reinterpret_cast<uint8_t*>(ws + s.records);
+    cudaError_t e = prepare(p, true, records, st);
+    if (e == cudaSuccess)
+        e = store_states(p, records, reinterpret_cast<float*>(ws + s.states), reinterpret_cast<float*>(ws + s.R),
+                         block_tokens(p) / C, st);
+    if (e == cudaSuccess)
+        e = reverse<E, DK>(p, gr, records, reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.H), st);
+    if (e == cudaSuccess) {
+        if (p.dv == 32) e = block_grads<E, DK, 32>(p, gr, ws, s, st);
+        else if (p.dv == 64) e = block_grads<E, DK, 64>(p, gr, ws, s, st);
+        else e = block_grads<E, DK, 128>(p, gr, ws, s, st);
+    }
+    if (e == cudaSuccess && p.H != p.Hk) {
+        const long long n = static_cast<long long>(p.B) * p.Hk * p.T * p.d / 4;
+        const long long want = (n + 255) / 256;
+        k_delta_share<E><<<static_cast<unsigned>(want < 148 * 16 ? want : 148 * 16), 256, 0, st>>>(
+            reinterpret_cast<float*>(ws + s.dq), reinterpret_cast<float*>(ws + s.dk), static_cast<E*>(gr.dq),
+            static_cast<E*>(gr.dk), p.B, p.Hk, p.H / p.Hk, p.T, p.d, p.bthd ? 1 : 0);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t backward_bytes(const Problem& p) { return space(p).end; }
+int backward_launches(const Problem& p) { return p.H != p.Hk ? 5 : 4; }
+
+cudaError_t backward(const Problem& p, const Gradients& gr, void* ws, cudaStream_t st) {
+    char* w = static_cast<char*>(ws);
+    if (p.bf16) {
+        if (p.d == 32) return all<bf16, 32>(p, gr, w, st);
+        if (p.d == 64) return all<bf16, 64>(p, gr, w, st);
+        return all<bf16, 128>(p, gr, w, st);
+    }
+    if (p.d == 32) return all<float, 32>(p, gr, w, st);
+    if (p.d == 64) return all<float, 64>(p, gr, w, st);
+    return all<float, 128>(p, gr, w, st);
+}
+
+}  // namespace delta
+}  // namespace hla

@@ -25,6 +25,9 @@ struct WalkArgs {
     void* o;
     float* state_out;         // after the last segment, or null
     float* sums;              // SUMMARY: [BH][segments - 1][d][dv + d]
+    float* states;            // STORE: [BH][blocks][d][dv], the state before each block of block_chunks chunks
+    float* errors;            // STORE: [BH][T][dv], R
+    int block_chunks;
     int Hk, H, T, dv, bthd;
     int segments, seg_chunks; // chunks of a segment
     float scale;
@@ -132,6 +135,18 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
             const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + ostage * F::OSTAGE + F::gates);
             uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 16) + part * (DH / 16)) * OT * 32 + lane;
             uint2* uf = reinterpret_cast<uint2*>(sm + F::uf + (c & 1) * F::UB) + grp * 2 * OT * 64 + lane * 2;
+            if (MODE == STORE) {
+                const int chunk = t_first / C + c;
+                if (chunk % a.block_chunks == 0) {
+                    const int blocks = ((a.T + C - 1) / C + a.block_chunks - 1) / a.block_chunks;
+                    float* to = a.states + (static_cast<long long>(bh) * blocks + chunk / a.block_chunks) * DK * a.dv +
+                                static_cast<long long>(part * DH + 2 * (lane & 3)) * a.dv + col0 + 16 * grp + (lane >> 2);
+#pragma unroll
+                    for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) to[static_cast<long long>(8 * n + (j & 1)) * a.dv + 8 * (j >> 1)] = S[n][j];
+                }
+            }
             // this part's share of S0^T K^T, all tokens
             float y[4][4] = {};
 #pragma unroll
@@ -227,7 +242,16 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
                 // U^T for the outputs, and U^T e^(c_C - c) for the state
                 float u[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = ((r[0][j] + r[1][j]) + (r[2][j] + r[3][j])) * ((j & 1) ? beta[e].y : beta[e].x);
+                for (int j = 0; j < 4; ++j) u[j] = (r[0][j] + r[1][j]) + (r[2][j] + r[3][j]);
+                if (MODE == STORE) {
+                    const int tok = t_first + c * C + 8 * n + 2 * (lane & 3);
+                    float* to = a.errors + (static_cast<long long>(bh) * a.T + tok) * a.dv + col0 + 16 * grp + (lane >> 2);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (tok + (j & 1) < t_end) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] *= (j & 1) ? beta[e].y : beta[e].x;
                 uint32_t t0[3], t1[3];
                 split<3>(u[0] * left[e].x, u[1] * left[e].y, t0);
                 split<3>(u[2] * left[e].x, u[3] * left[e].y, t1);
@@ -417,12 +441,36 @@ cudaError_t walk(const Problem& p, void* ws, cudaStream_t st) {
     uint8_t* records = static_cast<uint8_t*>(ws);
     cudaError_t e = prepare(p, false, records, st);
     if (e != cudaSuccess) return e;
-    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, p.o, p.state_out, nullptr,
+    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, p.o, p.state_out, nullptr, nullptr, nullptr, 1,
+               p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, 1, NC, p.scale};
+    return start<F>(a, BH * (p.dv / F::CS), st);
+}
+
+template <typename E, int DK>
+cudaError_t walk_store(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
+                       cudaStream_t st) {
+    constexpr int NG = sizeof(E) == 2 ? 2 : 1;
+    using F = Cfg<E, DK, NG, STORE>;
+    static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
+    const int BH = p.B * p.H, NC = (p.T + C - 1) / C;
+    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, nullptr, nullptr, nullptr, states, errors, block_chunks,
                p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, 1, NC, p.scale};
     return start<F>(a, BH * (p.dv / F::CS), st);
 }
 
 }  // namespace
+
+cudaError_t store_states(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
+                         cudaStream_t st) {
+    if (p.bf16) {
+        if (p.d == 32) return walk_store<bf16, 32>(p, records, states, errors, block_chunks, st);
+        if (p.d == 64) return walk_store<bf16, 64>(p, records, states, errors, block_chunks, st);
+        return walk_store<bf16, 128>(p, records, states, errors, block_chunks, st);
+    }
+    if (p.d == 32) return walk_store<float, 32>(p, records, states, errors, block_chunks, st);
+    if (p.d == 64) return walk_store<float, 64>(p, records, states, errors, block_chunks, st);
+    return walk_store<float, 128>(p, records, states, errors, block_chunks, st);
+}
 
 size_t forward_bytes(const Problem& p) { return records_bytes(p, false); }
 

@@ -26,7 +26,8 @@ _CODES = {torch.float32: HLA_F32, torch.bfloat16: HLA_BF16}
 
 # Every symbol include/hla_delta.h declares.
 EXPORTS = ("hla_delta_abi_version", "hla_delta_workspace_bytes", "hla_delta_kernel_launches", "hla_delta_forward",
-           "hla_delta_step", "hla_group_norm_forward", "hla_group_norm_backward_workspace_bytes",
+           "hla_delta_step", "hla_delta_backward_workspace_bytes", "hla_delta_backward_kernel_launches",
+           "hla_delta_backward", "hla_group_norm_forward", "hla_group_norm_backward_workspace_bytes",
            "hla_group_norm_backward")
 
 _bound = None
@@ -43,6 +44,9 @@ def _library():
                 ("hla_delta_workspace_bytes", sizes, sz),
                 ("hla_delta_kernel_launches", sizes, i),
                 ("hla_delta_forward", [vp] * 9 + [i] * 8 + [f, vp, sz, vp], i),
+                ("hla_delta_backward_workspace_bytes", sizes, sz),
+                ("hla_delta_backward_kernel_launches", sizes, i),
+                ("hla_delta_backward", [vp] * 15 + [i] * 8 + [f, vp, sz, vp], i),
                 ("hla_delta_step", [vp] * 7 + [i] * 6 + [f, vp], i),
                 ("hla_group_norm_forward", [vp] * 5 + [ll, i, i, i, f, i, vp], i),
                 ("hla_group_norm_backward_workspace_bytes", [i, ll, i, i], sz),
@@ -203,6 +207,44 @@ def gated_delta_step(state, q, k, v, g, beta, scale: Optional[float] = None, out
             k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), B, Hk, H, d, dv,
             _CODES[q.dtype], d ** -0.5 if scale is None else scale, on.handle)
     return out
+
+
+def gated_delta_backward_workspace_bytes(dtype, B: int, Hk: int, H: int, T: int, d: int, dv: int) -> int:
+    """Bytes of workspace :func:`gated_delta_backward` needs (0: no such call); ``dtype`` is torch's."""
+    return int(_library().hla_delta_backward_workspace_bytes(_CODES.get(dtype, -1), B, Hk, H, T, d, dv))
+
+
+def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, initial_state=None, dstate=None,
+                         lengths=None, layout: str = "bhtd", workspace=None, stream=None):
+    """Gradients (dq, dk, dv, dg, dbeta, dstate0) of ``sum(o * dout) + sum(state * dstate)`` for
+    ``o, state = gated_delta(q, k, v, g, beta, scale, initial_state, lengths, layout,
+    return_state=True)``.  dout is shaped and typed like v; ``dstate`` [B, H, d, dv] fp32 (default:
+    zeros).  dq, dk, dv come in the inputs' type, the others in fp32; dstate0 is None without an
+    initial state.  Nothing of the forward call is needed."""
+    B, Hk, H, T, d, dv = _leaves(q, k, v, g, beta, layout)
+    dev = q.device
+    _lengths(lengths, B, dev)
+    _expect("dout", dout, tuple(v.shape), v.dtype, dev)
+    for name, t in (("initial_state", initial_state), ("dstate", dstate)):
+        if t is not None:
+            _expect(name, t, (B, H, d, dv), torch.float32, dev)
+    on = _On(dev, stream)
+    lib = _library()
+    code = _CODES[q.dtype]
+    if workspace is None:
+        n = int(lib.hla_delta_backward_workspace_bytes(code, B, Hk, H, T, d, dv))
+        if n == 0:
+            raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    dq, dk, dvv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
+    dstate0 = torch.empty_like(initial_state) if initial_state is not None else None
+    on.keep(dq, dk, dvv, dg, dbeta, dstate0, workspace)
+    on.call(lib.hla_delta_backward, "hla_delta_backward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), dout.data_ptr(), _ptr(dstate),
+            dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dstate0), B, Hk, H, T, d,
+            dv, code, LAYOUTS[layout], d ** -0.5 if scale is None else scale, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), on.handle)
+    return dq, dk, dvv, dg, dbeta, dstate0
 
 
 # ---------------------------------------------------------------------------

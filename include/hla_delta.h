@@ -67,6 +67,25 @@ hla_status_t hla_delta_step(float* state, const void* q, const void* k, const vo
                             float scale, void* stream);
 
 /*
+ * Gradients of sum(o * dout) + sum(state_out * dstate_out) for the forward call of the same q, k,
+ * v, g, beta, state_in, lengths and scale (recomputed: nothing of the forward call is kept).
+ *   dout, dq, dk, dv_out: typed and laid out like o, q, k, v; dq and dk of a shared key head are the
+ *     sums over its value heads.  dg, dbeta: like g.  Rows behind a sequence's end get zeros.
+ *   dstate_out: [B][H][d][dv], or NULL for zeros.  dstate_in: the gradient at state_in, or NULL when
+ *     it is not wanted.
+ * The workspace holds about 1 kB a token and head at d = dv = 64 (bf16).  A fixed order of sums:
+ * the same inputs give the same bits.
+ */
+size_t hla_delta_backward_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv);
+int hla_delta_backward_kernel_launches(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv);
+hla_status_t hla_delta_backward(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                const float* state_in, const int* lengths, const void* dout,
+                                const float* dstate_out, void* dq, void* dk, void* dv_out, float* dg, float* dbeta,
+                                float* dstate_in, int B, int Hk, int H, int T, int d, int dv, hla_dtype_t dtype,
+                                hla_layout_t layout, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * Group norm with an activation over channels-last rows, each position by itself (the norm of a
  * linear-attention layer's heads: groups = heads).  x is [rows][C]; a group is C / groups
  * neighbouring channels of one row:

@@ -84,6 +84,31 @@ def test_step_argument_errors(lib):
     assert step(H=0) == SHAPE and step(Hk=3) == SHAPE and step(dtype=5) == DTYPE and step(d=65) == UNSUPPORTED
 
 
+def test_backward_argument_errors(lib):
+    ws = lib.hla_delta_backward_workspace_bytes
+    for dtype in (hla.HLA_F32, hla.HLA_BF16):
+        assert 0 < ws(dtype, 1, 2, 2, 1, 64, 64) <= ws(dtype, 1, 2, 2, 4096, 64, 64) < ws(dtype, 1, 1, 2, 4096, 64, 64)
+    assert lib.hla_delta_backward_kernel_launches(1, 1, 1, 2, 100, 64, 64) == 5    # shared heads: one more
+    assert lib.hla_delta_backward_kernel_launches(1, 1, 2, 2, 100, 64, 64) == 4
+    assert ws(1, 1, 2, 3, 1, 64, 64) == 0 and lib.hla_delta_backward_kernel_launches(1, 1, 1, 1, 1, 8, 64) == 0
+
+    def back(**kw):
+        a = dict(q=16, k=16, v=16, g=4, beta=4, state_in=0, lengths=0, dout=16, dstate_out=0, dq=16, dk=16, dv_out=16,
+                 dg=4, dbeta=4, dstate_in=0, B=1, Hk=1, H=2, T=8, d=64, dv=64, dtype=1, layout=0, scale=1.0, ws=16,
+                 wsb=1 << 40, stream=0)
+        a.update(kw)
+        return lib.hla_delta_backward(*a.values())
+
+    for n in ("q", "k", "v", "g", "beta", "dout", "dq", "dk", "dv_out", "dg", "dbeta"):
+        assert back(**{n: 0}) == NULL, n
+    for n in ("q", "k", "v", "dout", "dq", "dk", "dv_out", "state_in", "dstate_out", "dstate_in", "ws"):
+        assert back(**{n: 8}) == ALIGN, n
+    for n in ("g", "beta", "dg", "dbeta", "lengths"):
+        assert back(**{n: 2}) == ALIGN, n
+    assert back(H=0) == SHAPE and back(dtype=3) == DTYPE and back(dv=16) == UNSUPPORTED and back(layout=7) == UNSUPPORTED
+    assert back(ws=0) == WORKSPACE and back(wsb=1024) == WORKSPACE
+
+
 def test_norm_argument_errors(lib):
     def fwd(**kw):
         a = dict(x=16, gate=0, w=4, b=4, y=16, rows=3, C=64, groups=2, dtype=0, eps=1e-5, flags=0, s=0)
