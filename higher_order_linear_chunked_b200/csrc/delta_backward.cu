@@ -317,8 +317,13 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
 //     dq  = scale e^c dO S0^T + (scale D dO U^T) K
 //     dk  = -e^c Z S0^T + (-D Z U^T) K                                  (as a row of M)
 //         + e^(c_N - c) U dS^T + (scale D dO U^T)^T Q + (-D Z U^T)^T K    (as a column)
-// and the gradient at c, of which every term is a product already taken:
-//     dc_i = q_i . dq_i + k_i . dk_i(row) - k_i . dk_i(column),  dc_N += <dS, S behind the block>
+// A pair (i, j) depends on the decays through e^(c_i - c_j), that is on g of the tokens j < t <= i.
+// With x_ij what the pair contributes to the loss's logarithmic derivative, e_i the same of token i
+// against S0 and x_j of token j against dS,
+//     dg_t = sum_{j < t <= i} x_ij + sum_{i >= t} e_i + sum_{j < t} x_j + e^(c_N) <dS, S0>.
+// The first sum is the running sum of (row sum - column sum) of x: both from the same numbers, so
+// that what cancels there does so to the last bit (from q.dq - k.dk, the same in theory, dg came out
+// ten times less exact).
 struct BlockArgs {
     const void *q, *k, *dout;
     const float *g, *beta, *states, *dstates, *R, *H;
@@ -339,8 +344,8 @@ struct Blk {
     static constexpr int k = 0, q = k + KT * KTERM, o = q + KT * KTERM, u = o + KT * OTERM, z = u + 3 * OTERM;
     static constexpr int s = z + 3 * OTERM;
     static constexpr int sum = s + 3 * STERM, since = sum + N * 8, left = since + N * 4, beta = left + N * 4;
-    static constexpr int dc = beta + N * 4, red = dc + N * 4;
-    static constexpr int bytes = red + 64 * 4;
+    static constexpr int dc = beta + N * 4, xj = dc + N * 4, cols = xj + N * 4, red = cols + WARPS * N * 4;
+    static constexpr int bytes = red + 32 * 4;
 };
 
 // R rows x D columns of fp32 (times fac[row] where given) into three swizzled bf16 terms.
@@ -425,17 +430,34 @@ __device__ __forceinline__ void with_state(float (&acc)[F::DK / 8][4], uint32_t 
         __syncthreads();
         load_split<SW * 2, DK, SW, F::NT>(sb + F::s, F::STERM, state + c0, DV, DK, tid, nullptr);
         __syncthreads();
+        uint32_t x[SW / 16][AT][4];
 #pragma unroll
-        for (int ks = 0; ks < SW / 16; ++ks) {
-            uint32_t x[AT][4];
+        for (int ks = 0; ks < SW / 16; ++ks)
 #pragma unroll
-            for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
+            for (int t = 0; t < AT; ++t) ldsm4(x[ks][t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
 #pragma unroll
-            for (int np = 0; np < DK / 16; ++np) {
-                uint32_t y[3][4];
+        for (int np = 0; np < DK / 16; ++np) {
+            // a fresh sum, its smallest products first: every step cuts at the sum's last bit
+            uint32_t y[SW / 16][3][4];
+            float w[2][4] = {};
 #pragma unroll
-                for (int t = 0; t < 3; ++t) ldsm4(y[t], at_pieces_first<SW * 2>(sb + F::s + t * F::STERM, 16 * np, 2 * ks, lane));
-                prod2<AT, 3>(acc[2 * np], acc[2 * np + 1], x, y);
+            for (int ks = 0; ks < SW / 16; ++ks)
+#pragma unroll
+                for (int t = 0; t < 3; ++t) ldsm4(y[ks][t], at_pieces_first<SW * 2>(sb + F::s + t * F::STERM, 16 * np, 2 * ks, lane));
+#pragma unroll
+            for (int d = 2; d >= 0; --d)
+#pragma unroll
+                for (int ks = 0; ks < SW / 16; ++ks)
+#pragma unroll
+                    for (int i = 0; i < AT; ++i)
+                        if (i <= d) {
+                            mma16816(w[0], x[ks][i], y[ks][d - i][0], y[ks][d - i][1]);
+                            mma16816(w[1], x[ks][i], y[ks][d - i][2], y[ks][d - i][3]);
+                        }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[2 * np][j] += w[0][j];
+                acc[2 * np + 1][j] += w[1][j];
             }
         }
     }
@@ -444,9 +466,11 @@ __device__ __forceinline__ void with_state(float (&acc)[F::DK / 8][4], uint32_t 
 // acc += (f D o (X Y^T)) B over the 16 x 16 blocks of one side of the diagonal: X the rows of this
 // warp's tokens, Y and B rows of the whole block.  ROWS: this warp's tokens are i (D_ij counts for
 // j <= i, for j < i when STRICT), else they are j.
-template <typename F, int AT, int YT, bool ROWS, bool STRICT>
+// With ROWS also x = (f D o (X Y^T)) o (G B^T) for the rows G at `gt`: its row sums onto `rows`
+// and its column sums onto cols[warp][..] (FRESH: in their place).
+template <typename F, int AT, int YT, bool ROWS, bool STRICT, bool FRESH = false>
 __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t sb, const float2* sum, int at, int yt, int bt,
-                                           float f, int tid) {
+                                           float f, int tid, int gt = 0, float* rows = nullptr, float* cols = nullptr) {
     constexpr int DK = F::DK, DV = F::DV, KT = F::KT;
     const int lane = tid & 31, warp = tid >> 5, r0 = warp * 16;
 #pragma unroll 1
@@ -470,6 +494,34 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
                 const float2 x = sum[i], y = sum[k];
                 w[n][j] = (STRICT ? k < i : k <= i) ? f * w[n][j] * ex2((x.x - y.x) + (x.y - y.y)) : 0.f;
             }
+        if constexpr (ROWS) {
+            float g[2][4] = {};
+#pragma unroll 2
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                uint32_t x[KT][4], y[KT][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t) ldsm4(x[t], at_rows_first<DK * 2>(sb + gt + t * F::KTERM, r0, 2 * ks, lane));
+#pragma unroll
+                for (int t = 0; t < KT; ++t) ldsm4(y[t], at_pieces_first<DK * 2>(sb + bt + t * F::KTERM, 16 * jb, 2 * ks, lane));
+                prod2<KT, KT>(g[0], g[1], x, y);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    g[n][j] *= w[n][j];
+                    rows[j >> 1] += g[n][j];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float c = g[n][e] + g[n][2 + e];
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) c += __shfl_xor_sync(0xffffffffu, c, m);
+                    float* to = cols + warp * F::N + 16 * jb + 8 * n + 2 * lane + e;
+                    if (lane < 4) *to = FRESH ? c : *to + c;
+                }
+            }
+        }
         uint32_t x[3][4];
         split_a<3>(w[0], w[1], x);
 #pragma unroll
@@ -477,7 +529,13 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
             uint32_t y[KT][4];
 #pragma unroll
             for (int t = 0; t < KT; ++t) ldsm4t(y[t], at_rows_first<DK * 2>(sb + bt + t * F::KTERM, 16 * jb, 2 * np, lane));
-            prod2<3, KT>(acc[2 * np], acc[2 * np + 1], x, y);
+            float v[2][4] = {};
+            prod2<3, KT>(v[0], v[1], x, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[2 * np][j] += v[0][j];
+                acc[2 * np + 1][j] += v[1][j];
+            }
         }
     }
 }
@@ -533,6 +591,8 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
     float* left = reinterpret_cast<float*>(sm + F::left);
     float* beta = reinterpret_cast<float*>(sm + F::beta);
     float* dc = reinterpret_cast<float*>(sm + F::dc);
+    float* xj = reinterpret_cast<float*>(sm + F::xj);
+    float* cols = reinterpret_cast<float*>(sm + F::cols);
     float* red = reinterpret_cast<float*>(sm + F::red);
     const float* R = a.R + (static_cast<long long>(bh) * a.T + t0) * DV;
     const float* H = a.H + (static_cast<long long>(bh) * a.T + t0) * DV;
@@ -628,53 +688,65 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
     O* const dq = static_cast<O*>(a.dq) + out_at;
     O* const dk = static_cast<O*>(a.dk) + out_at;
     float acc[DK / 8][4], row_dk[DK / 8][4];
-    float dcs[2], d1[2], d2[2], d3[2];
+    float eq[2], ek[2], xs[2], pairs[2] = {};
     clear(acc);
     with_state<F, KT>(acc, sb, F::o, S0, tid);
     by_row(acc, since, a.scale, r0, lane);
-    with_pairs<F, KT, 3, true, false>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid);
+    row_dots<DK, KT>(acc, sm + F::q, F::KTERM, r0, lane, eq);
+    with_pairs<F, KT, 3, true, false, true>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid, F::q, pairs, cols);
     write_rows(acc, dq, out_step, r0, rows, out_rows, lane);
-    row_dots<DK, KT>(acc, sm + F::q, F::KTERM, r0, lane, dcs);
     clear(row_dk);
     with_state<F, 3>(row_dk, sb, F::z, S0, tid);
     by_row(row_dk, since, -1.f, r0, lane);
-    with_pairs<F, 3, 3, true, true>(row_dk, sb, sum, F::z, F::u, F::k, -1.f, tid);
-    row_dots<DK, KT>(row_dk, sm + F::k, F::KTERM, r0, lane, d1);       // k . dk(row)
-    // the column terms on their own: they leave dc with the other sign
+    row_dots<DK, KT>(row_dk, sm + F::k, F::KTERM, r0, lane, ek);
+    with_pairs<F, 3, 3, true, true>(row_dk, sb, sum, F::z, F::u, F::k, -1.f, tid, F::k, pairs, cols);
     clear(acc);
     with_state<F, 3>(acc, sb, F::u, dS, tid);
     by_row(acc, left, 1.f, r0, lane);
-    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, d2);          // the writes' part of <dS, S>
-    with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, tid);
-    with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, tid);
-    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, d3);          // k . dk(column)
+    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, xs);
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][j] += row_dk[n][j];
+    with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, tid);
+    with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, tid);
     write_rows(acc, dk, out_step, r0, rows, out_rows, lane);
-    if ((lane & 3) == 0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) dc[r0 + (lane >> 2) + 8 * e] = dcs[e] + d1[e] - d3[e];
+    for (int e = 0; e < 2; ++e) {
+        pairs[e] += __shfl_xor_sync(0xffffffffu, pairs[e], 1);
+        pairs[e] += __shfl_xor_sync(0xffffffffu, pairs[e], 2);
+        const int r = r0 + (lane >> 2) + 8 * e;
+        if ((lane & 3) == 0) {
+            dc[r] = pairs[e] + eq[e] + ek[e];
+            xj[r] = xs[e];
+        }
     }
-    float end = (lane & 3) == 0 ? d2[0] + d2[1] : 0.f;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) end += __shfl_xor_sync(0xffffffffu, end, w);
-    if (lane == 0) red[32 + warp] = end;
     __syncthreads();
     if (warp == 0) {
-        // dg_i = sum of dc from i on; the state behind the block counts as one more term at its end
-        float tail = 0.f, cr = 0.f;
+        float cross_all = 0.f;
 #pragma unroll
-        for (int i = 0; i < F::WARPS; ++i) {
-            cr += red[i];
-            tail += red[32 + i];
+        for (int i = 0; i < F::WARPS; ++i) cross_all += red[i];
+        float tail = 0.f, head = since[N - 1] * cross_all, above[N / 32];
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {                 // sums over j < t
+            const int r = 32 * i + lane;
+            float x = xj[r];
+            const float own = x;
+#pragma unroll
+            for (int w = 1; w < 32; w <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, x, w);
+                if (lane >= w) x += y;
+            }
+            above[i] = head + (x - own);
+            head += __shfl_sync(0xffffffffu, x, 31);
         }
-        tail = fmaf(since[N - 1], cr, tail);
 #pragma unroll
-        for (int i = N / 32 - 1; i >= 0; --i) {
+        for (int i = N / 32 - 1; i >= 0; --i) {            // sums over i >= t
             const int r = 32 * i + lane;
             float x = dc[r];
+#pragma unroll
+            for (int w = 0; w < F::WARPS; ++w)
+                if (w >= r / 16) x -= cols[w * N + r];
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
                 const float y = __shfl_down_sync(0xffffffffu, x, w);
@@ -682,7 +754,7 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
             }
             x += tail;
             tail = __shfl_sync(0xffffffffu, x, 0);
-            if (r < out_rows) a.dg[vr + static_cast<long long>(r) * vstep] = r < rows ? x : 0.f;
+            if (r < out_rows) a.dg[vr + static_cast<long long>(r) * vstep] = r < rows ? x + above[i] : 0.f;
         }
     }
 }

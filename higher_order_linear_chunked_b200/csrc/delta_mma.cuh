@@ -40,34 +40,38 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // c[n] += A B(n-tile n) for 2 NP tiles; b[np][t] = {tile 2 np k-low, k-high, tile 2 np + 1 k-low, k-high}.
 // The tiles of one pair of terms follow one another, so a tile's own chain of sums does not stall
-// them, and the leading terms come first: they are ready before the residuals are.
+// them; the smallest products come first, since each sum is cut at the accumulator's last bit.
 template <int AT, int BT, int NP>
 __device__ __forceinline__ void prod(float (&c)[2 * NP][4], const uint32_t (&a)[AT][4], const uint32_t (&b)[NP][BT][4]) {
     constexpr int M = AT > BT ? AT : BT;
 #pragma unroll
-    for (int i = 0; i < AT; ++i)
+    for (int d = M - 1; d >= 0; --d)
 #pragma unroll
-        for (int j = 0; j < BT; ++j)
-            if (i + j < M) {
+        for (int i = 0; i < AT; ++i) {
+            const int j = d - i;
+            if (j >= 0 && j < BT) {
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     mma16816(c[2 * p], a[i], b[p][j][0], b[p][j][1]);
                     mma16816(c[2 * p + 1], a[i], b[p][j][2], b[p][j][3]);
                 }
             }
+        }
 }
 template <int AT, int BT>
 __device__ __forceinline__ void prod2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[AT][4],
                                       const uint32_t (&b)[BT][4]) {
     constexpr int M = AT > BT ? AT : BT;
 #pragma unroll
-    for (int i = 0; i < AT; ++i)
+    for (int d = M - 1; d >= 0; --d)
 #pragma unroll
-        for (int j = 0; j < BT; ++j)
-            if (i + j < M) {
+        for (int i = 0; i < AT; ++i) {
+            const int j = d - i;
+            if (j >= 0 && j < BT) {
                 mma16816(c0, a[i], b[j][0], b[j][1]);
                 mma16816(c1, a[i], b[j][2], b[j][3]);
             }
+        }
 }
 
 // The bf16 terms of a pair, packed (x0 in the low half).
