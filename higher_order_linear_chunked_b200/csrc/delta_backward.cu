@@ -339,11 +339,11 @@ struct Blk {
     using Elem = E;
     static constexpr int DK = DK_, DV = DV_, N = N_, WARPS = N_ / 16, NT = WARPS * 32;
     static constexpr int KT = sizeof(E) == 2 ? 1 : 3;
-    static constexpr int SW = DV_ < 32 ? DV_ : 32;      // value columns of a state at a time
+    static constexpr int SW = NT * 32 < DK_ * 32 ? 16 : 32;   // value columns of a state at a time
     static constexpr int KTERM = N * DK * 2, OTERM = N * DV * 2, STERM = DK * SW * 2;
     static constexpr int k = 0, q = k + KT * KTERM, o = q + KT * KTERM, u = o + KT * OTERM, z = u + 3 * OTERM;
     static constexpr int s = z + 3 * OTERM;
-    static constexpr int sum = s + 3 * STERM, since = sum + N * 8, left = since + N * 4, beta = left + N * 4;
+    static constexpr int sum = s + 2 * 3 * STERM, since = sum + N * 8, left = since + N * 4, beta = left + N * 4;
     static constexpr int dc = beta + N * 4, xj = dc + N * 4, cols = xj + N * 4, red = cols + WARPS * N * 4;
     static constexpr int bytes = red + 32 * 4;
 };
@@ -419,46 +419,74 @@ __device__ __forceinline__ void row_dots(const float (&acc)[D / 8][4], const uin
     }
 }
 
-// acc[16 tokens][DK] += rows of `at` (AT terms) x state^T, the state in slices of SW columns (the
-// whole block takes part).
+// A slice of SW columns of a state, from device memory into registers and from there into one of the
+// two shared buffers as three terms.
+template <typename F>
+struct Slice {
+    static constexpr int P = F::SW / 4, U = F::DK * P / F::NT;
+    static_assert(F::DK * P % F::NT == 0, "whole rounds");
+    float4 x[U];
+    __device__ __forceinline__ void load(const float* state, int tid) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = tid + u * F::NT;
+            x[u] = *reinterpret_cast<const float4*>(state + (i / P) * F::DV + (i % P) * 4);
+        }
+    }
+    __device__ __forceinline__ void put(uint32_t to, int tid) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = tid + u * F::NT, r = i / P, c = i % P;
+            uint32_t lo[3], hi[3];
+            split<3>(x[u].x, x[u].y, lo);
+            split<3>(x[u].z, x[u].w, hi);
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + t * F::STERM + piece<F::SW * 2>(r, c >> 1) + (c & 1) * 8),
+                             "r"(lo[t]), "r"(hi[t]) : "memory");
+        }
+    }
+    __device__ __forceinline__ float dot(const Slice& o) const {
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            s += (x[u].x * o.x[u].x + x[u].y * o.x[u].y) + (x[u].z * o.x[u].z + x[u].w * o.x[u].w);
+        return s;
+    }
+};
+
+// acc[16 tokens][DK] += columns c0.. of the rows at `at` (AT terms) x (slice at `st`)^T
 template <typename F, int AT>
-__device__ __forceinline__ void with_state(float (&acc)[F::DK / 8][4], uint32_t sb, int at, const float* state, int tid) {
+__device__ __forceinline__ void with_slice(float (&acc)[F::DK / 8][4], uint32_t at, uint32_t st, int c0, int r0, int lane) {
     constexpr int DK = F::DK, DV = F::DV, SW = F::SW;
-    const int lane = tid & 31, r0 = (tid >> 5) * 16;
-#pragma unroll 1
-    for (int c0 = 0; c0 < DV; c0 += SW) {
-        __syncthreads();
-        load_split<SW * 2, DK, SW, F::NT>(sb + F::s, F::STERM, state + c0, DV, DK, tid, nullptr);
-        __syncthreads();
-        uint32_t x[SW / 16][AT][4];
+    uint32_t x[SW / 16][AT][4];
+#pragma unroll
+    for (int ks = 0; ks < SW / 16; ++ks)
+#pragma unroll
+        for (int t = 0; t < AT; ++t) ldsm4(x[ks][t], at_rows_first<DV * 2>(at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
+#pragma unroll
+    for (int np = 0; np < DK / 16; ++np) {
+        // a fresh sum, its smallest products first: every step cuts at the sum's last bit
+        uint32_t y[SW / 16][3][4];
+        float w[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < SW / 16; ++ks)
 #pragma unroll
-            for (int t = 0; t < AT; ++t) ldsm4(x[ks][t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
+            for (int t = 0; t < 3; ++t) ldsm4(y[ks][t], at_pieces_first<SW * 2>(st + t * F::STERM, 16 * np, 2 * ks, lane));
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-            // a fresh sum, its smallest products first: every step cuts at the sum's last bit
-            uint32_t y[SW / 16][3][4];
-            float w[2][4] = {};
+        for (int d = 2; d >= 0; --d)
 #pragma unroll
             for (int ks = 0; ks < SW / 16; ++ks)
 #pragma unroll
-                for (int t = 0; t < 3; ++t) ldsm4(y[ks][t], at_pieces_first<SW * 2>(sb + F::s + t * F::STERM, 16 * np, 2 * ks, lane));
+                for (int i = 0; i < AT; ++i)
+                    if (i <= d) {
+                        mma16816(w[0], x[ks][i], y[ks][d - i][0], y[ks][d - i][1]);
+                        mma16816(w[1], x[ks][i], y[ks][d - i][2], y[ks][d - i][3]);
+                    }
 #pragma unroll
-            for (int d = 2; d >= 0; --d)
-#pragma unroll
-                for (int ks = 0; ks < SW / 16; ++ks)
-#pragma unroll
-                    for (int i = 0; i < AT; ++i)
-                        if (i <= d) {
-                            mma16816(w[0], x[ks][i], y[ks][d - i][0], y[ks][d - i][1]);
-                            mma16816(w[1], x[ks][i], y[ks][d - i][2], y[ks][d - i][3]);
-                        }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[2 * np][j] += w[0][j];
-                acc[2 * np + 1][j] += w[1][j];
-            }
+        for (int j = 0; j < 4; ++j) {
+            acc[2 * np][j] += w[0][j];
+            acc[2 * np + 1][j] += w[1][j];
         }
     }
 }
@@ -632,22 +660,6 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
         }
     }
     __syncthreads();
-    // dv = Z and dbeta = R . H, a row a warp at a time; then U and Z for the products
-    for (int r = warp; r < out_rows; r += F::WARPS) {
-        const bool on = r < rows;
-        const float bt = beta[r];
-        E* dv = static_cast<E*>(a.dv) + (vr + static_cast<long long>(r) * vstep) * DV;
-        float s = 0.f;
-#pragma unroll
-        for (int c = lane; c < DV; c += 32) {
-            const float x = on ? H[static_cast<long long>(r) * DV + c] : 0.f, y = on ? R[static_cast<long long>(r) * DV + c] : 0.f;
-            s = fmaf(x, y, s);
-            store_elem(dv + c, on ? bt * x : 0.f);
-        }
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        if (lane == 0) a.dbeta[vr + static_cast<long long>(r) * vstep] = s;
-    }
     if (rows <= 0) {
         for (int i = tid; i < out_rows * DK; i += NT) {
             const int r = i / DK, c = i % DK;
@@ -661,25 +673,60 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
                 store_elem(static_cast<E*>(a.dk) + at, 0.f);
             }
         }
-        for (int r = tid; r < out_rows; r += NT) a.dg[vr + static_cast<long long>(r) * vstep] = 0.f;
+        for (int i = tid; i < out_rows * DV; i += NT)
+            store_elem(static_cast<E*>(a.dv) + (vr + static_cast<long long>(i / DV) * vstep) * DV + i % DV, 0.f);
+        for (int r = tid; r < out_rows; r += NT) {
+            a.dg[vr + static_cast<long long>(r) * vstep] = 0.f;
+            a.dbeta[vr + static_cast<long long>(r) * vstep] = 0.f;
+        }
         return;
     }
-    load_split<DV * 2, N, DV, NT>(sb + F::u, F::OTERM, R, DV, rows, tid, beta);
-    load_split<DV * 2, N, DV, NT>(sb + F::z, F::OTERM, H, DV, rows, tid, beta);
-    // <dS, S0>
-    float cross = 0.f;
-#pragma unroll 4
-    for (int i = tid * 4; i < DK * DV; i += NT * 4) {
-        float x[4], y[4];
-        load4(S0 + i, x);
-        load4(dS + i, y);
-        cross += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
-    }
+    Slice<F> s0;
+    s0.load(S0, tid);
+    // U = beta R and Z = beta H for the products, dv = Z, dbeta = R . H (DV / 4 lanes a row)
+    {
+        constexpr int P = DV / 4, U = 4;
+        static_assert(N * P % (NT * U) == 0, "whole rounds");
+#pragma unroll 1
+        for (int i0 = tid; i0 < N * P; i0 += NT * U) {
+            float4 x[U], y[U];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, w);
-    if (lane == 0) red[warp] = cross;
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * NT, r = i / P;
+                x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < rows) {
+                    x[u] = *reinterpret_cast<const float4*>(R + i * 4);
+                    y[u] = *reinterpret_cast<const float4*>(H + i * 4);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * NT, r = i / P, c = i % P;
+                const float w = beta[r];
+                float dot = (x[u].x * y[u].x + x[u].y * y[u].y) + (x[u].z * y[u].z + x[u].w * y[u].w);
+#pragma unroll
+                for (int m = 1; m < P; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                const float z[4] = {w * y[u].x, w * y[u].y, w * y[u].z, w * y[u].w};
+                if (r < out_rows) {
+                    store4(static_cast<E*>(a.dv) + (vr + static_cast<long long>(r) * vstep) * DV + c * 4, z);
+                    if (c == 0) a.dbeta[vr + static_cast<long long>(r) * vstep] = dot;
+                }
+                const uint32_t at = piece<DV * 2>(r, c >> 1) + (c & 1) * 8;
+                uint32_t lo[3], hi[3];
+                split<3>(z[0], z[1], lo);
+                split<3>(z[2], z[3], hi);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sb + F::z + t * F::OTERM + at), "r"(lo[t]), "r"(hi[t]) : "memory");
+                split<3>(w * x[u].x, w * x[u].y, lo);
+                split<3>(w * x[u].z, w * x[u].w, hi);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sb + F::u + t * F::OTERM + at), "r"(lo[t]), "r"(hi[t]) : "memory");
+            }
+        }
+    }
     cp_wait<0>();
-    __syncthreads();
 
     // where dq and dk go: the gradients, or this value head's share of them
     using O = std::conditional_t<PARTIAL, float, E>;
@@ -688,22 +735,48 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
     O* const dq = static_cast<O*>(a.dq) + out_at;
     O* const dk = static_cast<O*>(a.dk) + out_at;
     float acc[DK / 8][4], row_dk[DK / 8][4];
-    float eq[2], ek[2], xs[2], pairs[2] = {};
+    float eq[2], ek[2], xs[2], pairs[2] = {}, cross = 0.f;
+    constexpr int SLICES = DV / SW;
     clear(acc);
-    with_state<F, KT>(acc, sb, F::o, S0, tid);
+    clear(row_dk);
+    // S0 with dO and Z, a slice's successor on its way meanwhile
+#pragma unroll 1
+    for (int n = 0; n < SLICES; ++n) {
+        const uint32_t st = sb + F::s + (n & 1) * 3 * F::STERM;
+        s0.put(st, tid);
+        __syncthreads();
+        if (n + 1 < SLICES) s0.load(S0 + (n + 1) * SW, tid);
+        with_slice<F, KT>(acc, sb + F::o, st, n * SW, r0, lane);
+        with_slice<F, 3>(row_dk, sb + F::z, st, n * SW, r0, lane);
+    }
+    Slice<F> ds;
+    s0.load(S0, tid);
+    ds.load(dS, tid);
     by_row(acc, since, a.scale, r0, lane);
     row_dots<DK, KT>(acc, sm + F::q, F::KTERM, r0, lane, eq);
-    with_pairs<F, KT, 3, true, false, true>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid, F::q, pairs, cols);
-    write_rows(acc, dq, out_step, r0, rows, out_rows, lane);
-    clear(row_dk);
-    with_state<F, 3>(row_dk, sb, F::z, S0, tid);
     by_row(row_dk, since, -1.f, r0, lane);
     row_dots<DK, KT>(row_dk, sm + F::k, F::KTERM, r0, lane, ek);
+    with_pairs<F, KT, 3, true, false, true>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid, F::q, pairs, cols);
+    write_rows(acc, dq, out_step, r0, rows, out_rows, lane);
     with_pairs<F, 3, 3, true, true>(row_dk, sb, sum, F::z, F::u, F::k, -1.f, tid, F::k, pairs, cols);
     clear(acc);
-    with_state<F, 3>(acc, sb, F::u, dS, tid);
+#pragma unroll 1
+    for (int n = 0; n < SLICES; ++n) {
+        const uint32_t st = sb + F::s + ((SLICES + n) & 1) * 3 * F::STERM;
+        ds.put(st, tid);
+        cross += ds.dot(s0);
+        __syncthreads();
+        if (n + 1 < SLICES) {
+            s0.load(S0 + (n + 1) * SW, tid);
+            ds.load(dS + (n + 1) * SW, tid);
+        }
+        with_slice<F, 3>(acc, sb + F::u, st, n * SW, r0, lane);
+    }
     by_row(acc, left, 1.f, r0, lane);
     row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, xs);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, w);
+    if (lane == 0) red[warp] = cross;
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
