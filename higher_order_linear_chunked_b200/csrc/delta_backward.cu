@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
 }
 
 // ------------------------------------------------------------------ gradients of a block
-// A block of N tokens (c, D, e^c from the block's first token), S0 before it, dS behind it, a warp
-// to 16 tokens:
+// A block of N tokens (c, D, e^c from the block's first token), S0 before it, dS behind it, two warps
+// to 16 tokens, one for the terms of dP = dO U^T and of dS, one for those of dM = -Z U^T (each has
+// the pairs of a row and of a column of blocks, five blocks of 16 x 16 in all whatever its tokens):
 //     dq  = scale e^c dO S0^T + (scale D dO U^T) K
 //     dk  = -e^c Z S0^T + (-D Z U^T) K                                  (as a row of M)
 //         + e^(c_N - c) U dS^T + (scale D dO U^T)^T Q + (-D Z U^T)^T K    (as a column)
@@ -337,15 +338,18 @@ struct BlockArgs {
 template <typename E, int DK_, int DV_, int N_>
 struct Blk {
     using Elem = E;
-    static constexpr int DK = DK_, DV = DV_, N = N_, WARPS = N_ / 16, NT = WARPS * 32;
+    static constexpr int DK = DK_, DV = DV_, N = N_, WARPS = N_ / 16, NT = 2 * WARPS * 32;
     static constexpr int KT = sizeof(E) == 2 ? 1 : 3;
-    static constexpr int SW = NT * 32 < DK_ * 32 ? 16 : 32;   // value columns of a state at a time
+    static constexpr int SW = 32;                       // value columns of a state at a time
     static constexpr int KTERM = N * DK * 2, OTERM = N * DV * 2, STERM = DK * SW * 2;
     static constexpr int k = 0, q = k + KT * KTERM, o = q + KT * KTERM, u = o + KT * OTERM, z = u + 3 * OTERM;
     static constexpr int s = z + 3 * OTERM;
     static constexpr int sum = s + 2 * 3 * STERM, since = sum + N * 8, left = since + N * 4, beta = left + N * 4;
-    static constexpr int dc = beta + N * 4, xj = dc + N * 4, cols = xj + N * 4, red = cols + WARPS * N * 4;
+    static constexpr int dc = beta + N * 4, xj = dc + 2 * N * 4, cols = xj + N * 4, red = cols + 2 * WARPS * N * 4;
     static constexpr int bytes = red + 32 * 4;
+    static_assert(N * DK * 4 <= 2 * 3 * STERM, "a half of dk passes through the slices' place");
+    // two blocks an SM where shared memory and 128 registers a thread let them
+    static constexpr int BLOCKS = DK <= 64 && bytes <= 113 * 1024 ? 2 : 1;
 };
 
 // R rows x D columns of fp32 (times fac[row] where given) into three swizzled bf16 terms.
@@ -419,8 +423,8 @@ __device__ __forceinline__ void row_dots(const float (&acc)[D / 8][4], const uin
     }
 }
 
-// A slice of SW columns of a state, from device memory into registers and from there into one of the
-// two shared buffers as three terms.
+// A slice of SW columns of a state, from device memory into registers and from there into shared
+// memory as three terms.
 template <typename F>
 struct Slice {
     static constexpr int P = F::SW / 4, U = F::DK * P / F::NT;
@@ -459,34 +463,24 @@ struct Slice {
 template <typename F, int AT>
 __device__ __forceinline__ void with_slice(float (&acc)[F::DK / 8][4], uint32_t at, uint32_t st, int c0, int r0, int lane) {
     constexpr int DK = F::DK, DV = F::DV, SW = F::SW;
-    uint32_t x[SW / 16][AT][4];
 #pragma unroll
-    for (int ks = 0; ks < SW / 16; ++ks)
+    for (int ks = 0; ks < SW / 16; ++ks) {
+        uint32_t x[AT][4];
 #pragma unroll
-        for (int t = 0; t < AT; ++t) ldsm4(x[ks][t], at_rows_first<DV * 2>(at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
+        for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(at + t * F::OTERM, r0, c0 / 8 + 2 * ks, lane));
 #pragma unroll
-    for (int np = 0; np < DK / 16; ++np) {
-        // a fresh sum, its smallest products first: every step cuts at the sum's last bit
-        uint32_t y[SW / 16][3][4];
-        float w[2][4] = {};
+        for (int np = 0; np < DK / 16; ++np) {
+            // a fresh sum, its smallest products first: every step cuts at the sum's last bit
+            uint32_t y[3][4];
+            float w[2][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < SW / 16; ++ks)
+            for (int t = 0; t < 3; ++t) ldsm4(y[t], at_pieces_first<SW * 2>(st + t * F::STERM, 16 * np, 2 * ks, lane));
+            prod2<AT, 3>(w[0], w[1], x, y);
 #pragma unroll
-            for (int t = 0; t < 3; ++t) ldsm4(y[ks][t], at_pieces_first<SW * 2>(st + t * F::STERM, 16 * np, 2 * ks, lane));
-#pragma unroll
-        for (int d = 2; d >= 0; --d)
-#pragma unroll
-            for (int ks = 0; ks < SW / 16; ++ks)
-#pragma unroll
-                for (int i = 0; i < AT; ++i)
-                    if (i <= d) {
-                        mma16816(w[0], x[ks][i], y[ks][d - i][0], y[ks][d - i][1]);
-                        mma16816(w[1], x[ks][i], y[ks][d - i][2], y[ks][d - i][3]);
-                    }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc[2 * np][j] += w[0][j];
-            acc[2 * np + 1][j] += w[1][j];
+            for (int j = 0; j < 4; ++j) {
+                acc[2 * np][j] += w[0][j];
+                acc[2 * np + 1][j] += w[1][j];
+            }
         }
     }
 }
@@ -495,12 +489,12 @@ __device__ __forceinline__ void with_slice(float (&acc)[F::DK / 8][4], uint32_t 
 // warp's tokens, Y and B rows of the whole block.  ROWS: this warp's tokens are i (D_ij counts for
 // j <= i, for j < i when STRICT), else they are j.
 // With ROWS also x = (f D o (X Y^T)) o (G B^T) for the rows G at `gt`: its row sums onto `rows`
-// and its column sums onto cols[warp][..] (FRESH: in their place).
-template <typename F, int AT, int YT, bool ROWS, bool STRICT, bool FRESH = false>
+// and its column sums to cols[warp][..].
+template <typename F, int AT, int YT, bool ROWS, bool STRICT>
 __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t sb, const float2* sum, int at, int yt, int bt,
-                                           float f, int tid, int gt = 0, float* rows = nullptr, float* cols = nullptr) {
+                                           float f, int lane, int warp, int gt = 0, float* rows = nullptr, float* cols = nullptr) {
     constexpr int DK = F::DK, DV = F::DV, KT = F::KT;
-    const int lane = tid & 31, warp = tid >> 5, r0 = warp * 16;
+    const int r0 = warp * 16;
 #pragma unroll 1
     for (int jb = ROWS ? 0 : warp; jb <= (ROWS ? warp : F::WARPS - 1); ++jb) {
         float w[2][4] = {};
@@ -546,7 +540,7 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
 #pragma unroll
                     for (int m = 4; m < 32; m <<= 1) c += __shfl_xor_sync(0xffffffffu, c, m);
                     float* to = cols + warp * F::N + 16 * jb + 8 * n + 2 * lane + e;
-                    if (lane < 4) *to = FRESH ? c : *to + c;
+                    if (lane < 4) *to = c;
                 }
             }
         }
@@ -602,12 +596,13 @@ __device__ __forceinline__ void write_rows(const float (&acc)[NT_][4], O* to, lo
 }
 
 template <typename F, bool PARTIAL>
-__global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) {
+__global__ void __launch_bounds__(F::NT, F::BLOCKS) k_delta_block_grads(const BlockArgs a) {
     using E = typename F::Elem;
     constexpr int DK = F::DK, DV = F::DV, N = F::N, KT = F::KT, NT = F::NT, SW = F::SW;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = 16 * warp;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tile = warp % F::WARPS, r0 = 16 * tile;
+    const bool of_m = warp >= F::WARPS;
     const int bh = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
     const int b = bh / a.Hv, h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
     const int t0 = blk * N, T = length_of(a.lengths, b, a.T);
@@ -681,11 +676,12 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
         }
         return;
     }
-    Slice<F> s0;
+    Slice<F> s0, ds;
     s0.load(S0, tid);
+    ds.load(dS, tid);
     // U = beta R and Z = beta H for the products, dv = Z, dbeta = R . H (DV / 4 lanes a row)
     {
-        constexpr int P = DV / 4, U = 4;
+        constexpr int P = DV / 4, U = N * P / NT < 4 ? N * P / NT : 4;
         static_assert(N * P % (NT * U) == 0, "whole rounds");
 #pragma unroll 1
         for (int i0 = tid; i0 < N * P; i0 += NT * U) {
@@ -734,71 +730,74 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
     const long long out_step = static_cast<long long>(PARTIAL ? 1 : kstep) * DK;
     O* const dq = static_cast<O*>(a.dq) + out_at;
     O* const dk = static_cast<O*>(a.dk) + out_at;
-    float acc[DK / 8][4], row_dk[DK / 8][4];
-    float eq[2], ek[2], xs[2], pairs[2] = {}, cross = 0.f;
-    constexpr int SLICES = DV / SW;
+    float acc[DK / 8][4], acc_q[DK / 8][4];          // a part of dk; dq
+    float cross = 0.f;
     clear(acc);
-    clear(row_dk);
-    // S0 with dO and Z, a slice's successor on its way meanwhile
+    clear(acc_q);
+    const uint32_t st0 = sb + F::s, st1 = st0 + 3 * F::STERM;
 #pragma unroll 1
-    for (int n = 0; n < SLICES; ++n) {
-        const uint32_t st = sb + F::s + (n & 1) * 3 * F::STERM;
-        s0.put(st, tid);
-        __syncthreads();
-        if (n + 1 < SLICES) s0.load(S0 + (n + 1) * SW, tid);
-        with_slice<F, KT>(acc, sb + F::o, st, n * SW, r0, lane);
-        with_slice<F, 3>(row_dk, sb + F::z, st, n * SW, r0, lane);
-    }
-    Slice<F> ds;
-    s0.load(S0, tid);
-    ds.load(dS, tid);
-    by_row(acc, since, a.scale, r0, lane);
-    row_dots<DK, KT>(acc, sm + F::q, F::KTERM, r0, lane, eq);
-    by_row(row_dk, since, -1.f, r0, lane);
-    row_dots<DK, KT>(row_dk, sm + F::k, F::KTERM, r0, lane, ek);
-    with_pairs<F, KT, 3, true, false, true>(acc, sb, sum, F::o, F::u, F::k, a.scale, tid, F::q, pairs, cols);
-    write_rows(acc, dq, out_step, r0, rows, out_rows, lane);
-    with_pairs<F, 3, 3, true, true>(row_dk, sb, sum, F::z, F::u, F::k, -1.f, tid, F::k, pairs, cols);
-    clear(acc);
-#pragma unroll 1
-    for (int n = 0; n < SLICES; ++n) {
-        const uint32_t st = sb + F::s + ((SLICES + n) & 1) * 3 * F::STERM;
-        ds.put(st, tid);
+    for (int n = 0; n < DV / SW; ++n) {
+        s0.put(st0, tid);
+        ds.put(st1, tid);
         cross += ds.dot(s0);
         __syncthreads();
-        if (n + 1 < SLICES) {
+        if (n + 1 < DV / SW) {                     // the next slices are on their way meanwhile
             s0.load(S0 + (n + 1) * SW, tid);
             ds.load(dS + (n + 1) * SW, tid);
         }
-        with_slice<F, 3>(acc, sb + F::u, st, n * SW, r0, lane);
+        if (of_m) {
+            with_slice<F, 3>(acc, sb + F::z, st0, n * SW, r0, lane);
+        } else {
+            with_slice<F, KT>(acc_q, sb + F::o, st0, n * SW, r0, lane);
+            with_slice<F, 3>(acc, sb + F::u, st1, n * SW, r0, lane);
+        }
+        __syncthreads();
     }
-    by_row(acc, left, 1.f, r0, lane);
-    row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, xs);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, w);
     if (lane == 0) red[warp] = cross;
+    float4* const pass = reinterpret_cast<float4*>(sm + F::s) + tile * (DK / 8) * 32 + lane;
+    float state_part[2], pairs[2] = {};
+    if (of_m) {
+        by_row(acc, since, -1.f, r0, lane);
+        row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, state_part);
+        with_pairs<F, 3, 3, true, true>(acc, sb, sum, F::z, F::u, F::k, -1.f, lane, tile, F::k, pairs, cols + F::WARPS * N);
+        with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, lane, tile);
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+        for (int n = 0; n < DK / 8; ++n) pass[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+    } else {
+        by_row(acc_q, since, a.scale, r0, lane);
+        row_dots<DK, KT>(acc_q, sm + F::q, F::KTERM, r0, lane, state_part);
+        with_pairs<F, KT, 3, true, false>(acc_q, sb, sum, F::o, F::u, F::k, a.scale, lane, tile, F::q, pairs, cols);
+        write_rows(acc_q, dq, out_step, r0, rows, out_rows, lane);
+        float xs[2];
+        by_row(acc, left, 1.f, r0, lane);
+        row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, xs);
+        with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, lane, tile);
+        if ((lane & 3) == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[n][j] += row_dk[n][j];
-    with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, tid);
-    with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, tid);
-    write_rows(acc, dk, out_step, r0, rows, out_rows, lane);
+            for (int e = 0; e < 2; ++e) xj[r0 + (lane >> 2) + 8 * e] = xs[e];
+        }
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         pairs[e] += __shfl_xor_sync(0xffffffffu, pairs[e], 1);
         pairs[e] += __shfl_xor_sync(0xffffffffu, pairs[e], 2);
-        const int r = r0 + (lane >> 2) + 8 * e;
-        if ((lane & 3) == 0) {
-            dc[r] = pairs[e] + eq[e] + ek[e];
-            xj[r] = xs[e];
-        }
+        if ((lane & 3) == 0) dc[(of_m ? N : 0) + r0 + (lane >> 2) + 8 * e] = pairs[e] + state_part[e];
     }
     __syncthreads();
-    if (warp == 0) {
+    if (!of_m) {
+#pragma unroll
+        for (int n = 0; n < DK / 8; ++n) {
+            const float4 x = pass[n * 32];
+            acc[n][0] += x.x; acc[n][1] += x.y; acc[n][2] += x.z; acc[n][3] += x.w;
+        }
+        write_rows(acc, dk, out_step, r0, rows, out_rows, lane);
+    }
+    if (warp == F::WARPS) {
         float cross_all = 0.f;
 #pragma unroll
-        for (int i = 0; i < F::WARPS; ++i) cross_all += red[i];
+        for (int i = 0; i < 2 * F::WARPS; ++i) cross_all += red[i];
         float tail = 0.f, head = since[N - 1] * cross_all, above[N / 32];
 #pragma unroll
         for (int i = 0; i < N / 32; ++i) {                 // sums over j < t
@@ -816,10 +815,10 @@ __global__ void __launch_bounds__(F::NT) k_delta_block_grads(const BlockArgs a) 
 #pragma unroll
         for (int i = N / 32 - 1; i >= 0; --i) {            // sums over i >= t
             const int r = 32 * i + lane;
-            float x = dc[r];
+            float x = dc[r] + dc[N + r];
 #pragma unroll
             for (int w = 0; w < F::WARPS; ++w)
-                if (w >= r / 16) x -= cols[w * N + r];
+                if (w >= r / 16) x -= cols[w * N + r] + cols[(F::WARPS + w) * N + r];
 #pragma unroll
             for (int w = 1; w < 32; w <<= 1) {
                 const float y = __shfl_down_sync(0xffffffffu, x, w);
