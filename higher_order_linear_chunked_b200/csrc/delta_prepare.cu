@@ -24,10 +24,12 @@ struct Prep {
     static constexpr int DK = DK_, PT = PT_, INV = INV_, KT = sizeof(E) == 2 ? 1 : 3;
     static constexpr int TILE = KT * C * DK * 2;
     static constexpr int REC = record_bytes(INV, PT);
-    // shared memory of one warp
-    static constexpr int k = 0, q = k + TILE, m = q + TILE, rec = m + C * kMS * 4, sum = rec + REC;
-    static constexpr int bytes = sum + C * 8;
-    static constexpr int WARPS = bytes > 56 * 1024 ? 2 : 4;
+    // shared memory of one warp: the inverse takes the queries' place once P is there, one inverse
+    // at a time; what the record has beside the inverses is staged behind
+    static constexpr int k = 0, q = k + TILE, x = q, m = q + (TILE > kXBytes ? TILE : kXBytes), p = m + C * kMS * 4;
+    static constexpr int TAIL = PT * C * C * 2 + 512, sum = p + TAIL;
+    static constexpr int bytes = (sum + C * 8 + 127) / 128 * 128;
+    static constexpr int WARPS = 2;              // small blocks: ten warps an SM at d = 64, bf16
 };
 
 template <typename F>
@@ -53,31 +55,42 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
     const bool on = lane < rows;
     const float g = on ? a.g[vr + static_cast<long long>(lane) * vstep] : 0.f;
     const float beta = on ? a.beta[vr + static_cast<long long>(lane) * vstep] : 0.f;
-    uint8_t* rec = sm + F::rec;
-    uint8_t* pt = rec + F::INV * kXBytes;
+    uint8_t* const pt = sm + F::p;
+    uint8_t* const xt = sm + F::x;
     Gates* gates = reinterpret_cast<Gates*>(pt + PT * C * C * 2);
     float2* sum = reinterpret_cast<float2*>(sm + F::sum);
     float* mt = reinterpret_cast<float*>(sm + F::m);
+    uint8_t* const rec = a.records + n * F::REC;
     finish_gates(gates, sum, g, beta, lane);
     // the blocks above the diagonal, which the products do not write
-#pragma unroll
-    for (int t = 0; t < F::INV * 3 + PT; ++t)
-        *reinterpret_cast<uint4*>(rec + t * (C * C * 2) + piece<C * 2>(lane & 15, 2 + (lane >> 4))) = make_uint4(0u, 0u, 0u, 0u);
+    const auto clear_above = [&](uint8_t* to, int terms) {
+        for (int t = 0; t < terms; ++t)
+            *reinterpret_cast<uint4*>(to + t * (C * C * 2) + piece<C * 2>(lane & 15, 2 + (lane >> 4))) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    clear_above(pt, PT);
     cp_wait<0>();
     __syncwarp();
 #pragma unroll 1
+    for (int w = 0; w < 2; ++w)
+        products<DK, KT, PT>(false, false, sb + F::k, sb + F::q, sum, gates->beta, mt, pt, a.scale, w, lane);
+    __syncwarp();
+    clear_above(xt, 3);
+    uint4* to = reinterpret_cast<uint4*>(rec + F::INV * kXBytes);
+#pragma unroll 4
+    for (int i = lane; i < F::TAIL / 16; i += 32) to[i] = reinterpret_cast<const uint4*>(pt)[i];
+#pragma unroll 1
     for (int x = 0; x < F::INV; ++x) {
 #pragma unroll 1
-        for (int w = 0; w < (x == 0 ? 4 : 2); ++w)      // keys (both halves), then queries
-            products<DK, KT, PT>(w < 2, x == 1, sb + F::k, sb + (w < 2 ? F::k : F::q), sum, gates->beta, mt, pt, a.scale,
-                                 w & 1, lane);
+        for (int w = 0; w < 2; ++w)
+            products<DK, KT, PT>(true, x == 1, sb + F::k, sb + F::k, sum, gates->beta, mt, pt, a.scale, w, lane);
         __syncwarp();
-        invert(mt, rec + x * kXBytes, lane);
+        invert(mt, xt, lane);
+        __syncwarp();
+        to = reinterpret_cast<uint4*>(rec + x * kXBytes);
+#pragma unroll 4
+        for (int i = lane; i < kXBytes / 16; i += 32) to[i] = reinterpret_cast<const uint4*>(xt)[i];
         __syncwarp();
     }
-    uint4* to = reinterpret_cast<uint4*>(a.records + n * F::REC);
-#pragma unroll 4
-    for (int i = lane; i < F::REC / 16; i += 32) to[i] = reinterpret_cast<const uint4*>(rec)[i];
 }
 
 template <typename E, int DK, int PT, int INV>

@@ -23,7 +23,7 @@ struct RecurArgs {
 };
 
 template <typename E, int DK, int CV, int NT>
-__global__ void __launch_bounds__(NT) k_delta_recur(const RecurArgs a) {
+__global__ void __launch_bounds__(NT, 1024 / NT) k_delta_recur(const RecurArgs a) {
     constexpr int LPR = CV / 4;           // lanes per state row (four columns each)
     constexpr int RPP = NT / LPR;         // rows per pass
     constexpr int NP = DK / RPP;          // passes: rows of one thread

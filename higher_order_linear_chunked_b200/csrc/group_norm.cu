@@ -27,15 +27,20 @@ template <> struct Raw<8> { using type = uint2; };
 template <> struct Raw<4> { using type = uint32_t; };
 template <> struct Raw<2> { using type = uint16_t; };
 
-// VEC elements at p as one load or store.
+// VEC elements as one load or store.
 template <typename E, int VEC>
-__device__ __forceinline__ void load(const E* p, float (&x)[VEC]) {
+struct Pack {
     using R = typename Raw<sizeof(E) * VEC>::type;
-    union { R r; E e[VEC]; } u;
-    u.r = *reinterpret_cast<const R*>(p);
+    R r;
+    __device__ __forceinline__ void load(const E* p) { r = *reinterpret_cast<const R*>(p); }
+    __device__ __forceinline__ void clear() { r = R{}; }
+    __device__ __forceinline__ void get(float (&x)[VEC]) const {
+        union { R r; E e[VEC]; } u;
+        u.r = r;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = to_f32(u.e[i]);
-}
+        for (int i = 0; i < VEC; ++i) x[i] = to_f32(u.e[i]);
+    }
+};
 __device__ __forceinline__ void round_to(float& e, float x) { e = x; }
 __device__ __forceinline__ void round_to(bf16& e, float x) { e = __float2bfloat16_rn(x); }
 template <typename E, int VEC>
@@ -46,12 +51,36 @@ __device__ __forceinline__ void store(E* p, const float (&x)[VEC]) {
     for (int i = 0; i < VEC; ++i) round_to(u.e[i], x[i]);
     *reinterpret_cast<R*>(p) = u.r;
 }
+// VEC floats of a per-channel vector (4-byte aligned only when VEC is 1; its base is 16-byte aligned
+// when `wide`), or `none` where there is no vector.
+template <int VEC>
+__device__ __forceinline__ void channel(const float* p, int at, bool wide, float none, float (&x)[VEC]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = none;
+    } else if (VEC % 4 == 0 && wide) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + at + i);
+            x[i] = v.x; x[i + 1 < VEC ? i + 1 : i] = v.y; x[i + 2 < VEC ? i + 2 : i] = v.z; x[i + 3 < VEC ? i + 3 : i] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = p[at + i];
+    }
+}
 
 __device__ __forceinline__ float lanes_sum(float x, int L) {
     for (int w = 1; w < L; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
     return x;
 }
-__device__ __forceinline__ float sigmoid(float a) { return 1.f / (1.f + expf(-a)); }
+// 1 / (1 + e^-a): for fp32 by the library's exponential and division, for bf16 (a result of eight
+// bits) by the approximate ones, whose 2^-21 it does not see.
+template <typename E>
+__device__ __forceinline__ float sigmoid(float a) {
+    if constexpr (sizeof(E) == 2) return __fdividef(1.f, 1.f + __expf(-a));
+    else return 1.f / (1.f + expf(-a));
+}
 
 // n of one group in place of x; returns r.  Lanes past the width hold zeros before and after.
 template <int VEC, int IT>
@@ -85,52 +114,67 @@ __device__ __forceinline__ float normalise(float (&x)[IT][VEC], const bool (&on)
 
 constexpr int kThreads = 256;
 
+// Two groups to a group of lanes, half the grid apart in memory order (both in flight at once).
 template <typename E, int VEC, int IT>
-__global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int L) {
+__global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int L, bool wide) {
+    constexpr int U = IT * VEC <= 8 ? 2 : 1;
     const int width = a.C / a.groups;
     const long long total = a.rows * a.groups;
     const int lane = threadIdx.x & 31;
     const int sub = lane / L, in = lane % L;
-    const long long gi = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 / L) + sub;
-    const bool live = gi < total;                       // whole groups of lanes; shuffles need every lane
-    const long long base = (live ? gi : 0) * width;
-    const int wbase = static_cast<int>((live ? gi : 0) % a.groups) * width;
-    float x[IT][VEC], t[IT][VEC];
-    bool on[IT];
+    const int per = 32 / L;                                  // groups of lanes in a warp
+    const long long first = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (per * U) + sub;
+    Pack<E, VEC> rx[U][IT], rt[U][IT];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int e = (i * L + in) * VEC;
-        on[i] = live && e < width;
-        if (on[i]) load<E, VEC>(static_cast<const E*>(a.x) + base + e, x[i]);
-        if (on[i] && a.gate) load<E, VEC>(static_cast<const E*>(a.gate) + base + e, t[i]);
-        if (!on[i]) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) x[i][j] = 0.f;
+        for (int i = 0; i < IT; ++i) {
+            const long long gi = first + u * per;
+            const int e = (i * L + in) * VEC;
+            if (gi < total && e < width) {
+                rx[u][i].load(static_cast<const E*>(a.x) + gi * width + e);
+                if (a.gate) rt[u][i].load(static_cast<const E*>(a.gate) + gi * width + e);
+            } else {
+                rx[u][i].clear();
+            }
         }
-    }
-    normalise<VEC, IT>(x, on, L, width, a.eps, a.center);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        if (!on[i]) continue;
-        const int e = (i * L + in) * VEC;
-        float out[VEC];
+    for (int u = 0; u < U; ++u) {
+        const long long gi = first + u * per;
+        const bool live = gi < total;                        // every lane takes part in the shuffles
+        const int wbase = static_cast<int>((live ? gi : 0) % a.groups) * width;
+        float x[IT][VEC];
+        bool on[IT];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float z = x[i][j];
-            if (a.weight) z *= a.weight[wbase + e + j];
-            if (a.bias) z += a.bias[wbase + e + j];
-            const float hot = a.gate ? t[i][j] : z;
-            const float act = a.silu ? hot * sigmoid(hot) : hot;
-            out[j] = a.gate ? z * act : act;
+        for (int i = 0; i < IT; ++i) {
+            on[i] = live && (i * L + in) * VEC < width;
+            rx[u][i].get(x[i]);
         }
-        store<E, VEC>(static_cast<E*>(a.y) + base + e, out);
+        normalise<VEC, IT>(x, on, L, width, a.eps, a.center);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (!on[i]) continue;
+            const int e = (i * L + in) * VEC;
+            float out[VEC], t[VEC], w[VEC], b[VEC];
+            channel<VEC>(a.weight, wbase + e, wide, 1.f, w);
+            channel<VEC>(a.bias, wbase + e, wide, 0.f, b);
+            if (a.gate) rt[u][i].get(t);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float z = fmaf(x[i][j], w[j], b[j]);
+                const float hot = a.gate ? t[j] : z;
+                const float act = a.silu ? hot * sigmoid<E>(hot) : hot;
+                out[j] = a.gate ? z * act : act;
+            }
+            store<E, VEC>(static_cast<E*>(a.y) + gi * width + e, out);
+        }
     }
 }
 
-// A group of lanes keeps one group column and walks the rows slot, slot + slots, ...; its sums over
-// those rows go to row `slot` of the partial sums.
+// A group of lanes keeps one group column and walks the rows slot, slot + slots, ..., the next row on
+// its way while it works on one; its sums over those rows go to row `slot` of the partial sums.
 template <typename E, int VEC, int IT>
-__global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int L, int slots) {
+__global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int L, int slots, bool wide) {
     const int width = a.C / a.groups;
     const int lane = threadIdx.x & 31;
     const int sub = lane / L, in = lane % L;
@@ -144,36 +188,44 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
     for (int i = 0; i < IT; ++i) {
         const int e = (i * L + in) * VEC;
         on[i] = mine && e < width;
+        channel<VEC>(on[i] ? a.weight : nullptr, wbase + e, wide, 1.f, w[i]);
+        channel<VEC>(on[i] ? a.bias : nullptr, wbase + e, wide, 0.f, bb[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            w[i][j] = (on[i] && a.weight) ? a.weight[wbase + e + j] : 1.f;
-            bb[i][j] = (on[i] && a.bias) ? a.bias[wbase + e + j] : 0.f;
-            dw[i][j] = 0.f;
-            db[i][j] = 0.f;
-        }
+        for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.f;
     }
     const float inv = 1.f / static_cast<float>(width);
-    // every lane group of a warp makes the same number of rounds: shuffles need every lane
+    // every group of lanes of a warp makes the same number of rounds: shuffles need every lane
     const long long rounds = (a.rows + slots - 1) / slots;
+    Pack<E, VEC> rx[IT], rd[IT], rt[IT];
+    const auto ask = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (on[i] && row < a.rows) {
+                const long long at = row * a.C + wbase + (i * L + in) * VEC;
+                rx[i].load(static_cast<const E*>(a.x) + at);
+                rd[i].load(static_cast<const E*>(a.dy) + at);
+                if (a.gate) rt[i].load(static_cast<const E*>(a.gate) + at);
+            } else {
+                rx[i].clear();
+                rd[i].clear();
+                rt[i].clear();
+            }
+        }
+    };
+    ask(slot);
     for (long long n = 0; n < rounds; ++n) {
         const long long row = n * slots + slot;
-        const bool live = mine && row < a.rows;
-        const long long base = (live ? row : 0) * a.C + wbase;
+        const long long base = row * a.C + wbase;
         float x[IT][VEC], t[IT][VEC], dz[IT][VEC];
         bool here[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int e = (i * L + in) * VEC;
-            here[i] = live && on[i];
-            if (here[i]) {
-                load<E, VEC>(static_cast<const E*>(a.x) + base + e, x[i]);
-                load<E, VEC>(static_cast<const E*>(a.dy) + base + e, dz[i]);
-                if (a.gate) load<E, VEC>(static_cast<const E*>(a.gate) + base + e, t[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) x[i][j] = 0.f, dz[i][j] = 0.f, t[i][j] = 0.f;
-            }
+            here[i] = on[i] && row < a.rows;
+            rx[i].get(x[i]);
+            rd[i].get(dz[i]);
+            if (a.gate) rt[i].get(t[i]);
         }
+        ask(row + slots);
         const float r = normalise<VEC, IT>(x, here, L, width, a.eps, a.center);
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
@@ -185,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
                 const float hot = a.gate ? t[i][j] : z;
                 float act = hot, slope = 1.f;
                 if (a.silu) {
-                    const float s = sigmoid(hot);
+                    const float s = sigmoid<E>(hot);
                     act = hot * s;
                     slope = s * (1.f + hot * (1.f - s));
                 }
@@ -265,17 +317,22 @@ Shape shape_of(bool is_bf16, int width) {
     return s;
 }
 
+// weight and bias on 16 bytes (the C ABI asks for 4 only)
+bool wide_channels(const Args& a) {
+    return ((reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
+}
+
 template <typename E, int VEC, int IT>
 void run_forward(const Args& a, int L, cudaStream_t st) {
-    const long long per = (kThreads / 32) * (32 / L);
+    const long long per = (kThreads / 32) * (32 / L) * (IT * VEC <= 8 ? 2 : 1);
     const long long blocks = (a.rows * a.groups + per - 1) / per;
-    k_group_norm<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L);
+    k_group_norm<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L, wide_channels(a));
 }
 template <typename E, int VEC, int IT>
 void run_backward(const Args& a, int L, int slots, cudaStream_t st) {
     const long long per = (kThreads / 32) * (32 / L);
     const long long blocks = (static_cast<long long>(slots) * a.groups + per - 1) / per;
-    k_group_norm_grad<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L, slots);
+    k_group_norm_grad<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L, slots, wide_channels(a));
 }
 
 template <typename F>

@@ -61,17 +61,21 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
     """The device and stream of one call: the tensors' device is made current for it, and what the
     call allocates is kept for the stream that uses it."""
 
+    __slots__ = ("device", "given", "handle")
+
     def __init__(self, device, stream):
         self.device, self.given = device, stream
-        self.handle = (stream.cuda_stream if stream is not None
-                       else torch.cuda.current_stream(device).cuda_stream)
+        self.handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
 
     def keep(self, *tensors):
-        if self.given is not None and self.handle != torch.cuda.current_stream(self.device).cuda_stream:
+        if self.given is not None and self.handle != _raw_stream(self.device.index):
             for t in tensors:
                 if t is not None:
                     t.record_stream(self.given)
@@ -125,11 +129,15 @@ def _leaves(q, k, v, g, beta, layout, step=False):
         lead = (B, T, H)
     else:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
-    _expect("q", q, tuple(q.shape), dt, dev)
-    _expect("k", k, tuple(q.shape), dt, dev)
-    _expect("v", v, (*lead, dv), dt, dev)
-    _expect("g", g, lead, torch.float32, dev)
-    _expect("beta", beta, lead, torch.float32, dev)
+    if not (k.shape == q.shape and v.shape == (*lead, dv) and g.shape == lead and beta.shape == lead and
+            k.dtype is dt and v.dtype is dt and g.dtype is torch.float32 and beta.dtype is torch.float32 and
+            k.device == dev and v.device == dev and g.device == dev and beta.device == dev and q.is_contiguous() and
+            k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
+        _expect("q", q, tuple(q.shape), dt, dev)
+        _expect("k", k, tuple(q.shape), dt, dev)
+        _expect("v", v, (*lead, dv), dt, dev)
+        _expect("g", g, lead, torch.float32, dev)
+        _expect("beta", beta, lead, torch.float32, dev)
     if min(B, Hk, H, T, d, dv) < 1:
         raise HLAError(2, f"an empty axis: B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
     if H % Hk:
