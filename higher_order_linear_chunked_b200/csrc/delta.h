@@ -62,6 +62,10 @@ struct Args {
     long long rows;
     int C, groups, center, silu;
     float eps;
+    // filled in on the way to the kernels: channels of a group and their reciprocal, and how far a
+    // row's groups move on from one of a warp's sets of groups to the next
+    int width, advance;
+    float inv;
 };
 
 constexpr int kMaxWidth = 512;   // channels of a group

@@ -22,9 +22,9 @@ static_assert(sizeof(Gates) == 512, "a record's last piece");
 constexpr int kXBytes = 3 * C * C * 2;
 constexpr int record_bytes(int inverses, int PT) { return inverses * kXBytes + PT * C * C * 2 + 512; }
 
-__device__ __forceinline__ float ex2(float x) {      // 2^x to 2^-22
+__device__ __forceinline__ float ex2(float x) {      // 2^x to 2^-22, below 2^-126 zero
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // 2^x, the whole part apart from the rest: a rounding of a large x costs nothing

@@ -78,15 +78,21 @@ __device__ __forceinline__ float lanes_sum(float x, int L) {
 // bits) by the approximate ones, whose 2^-21 it does not see.
 template <typename E>
 __device__ __forceinline__ float sigmoid(float a) {
-    if constexpr (sizeof(E) == 2) return __fdividef(1.f, 1.f + __expf(-a));
-    else return 1.f / (1.f + expf(-a));
+    if constexpr (sizeof(E) == 2) {
+        float e, s;                              // e^-a as 2^(-a / ln 2)
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+        return s;
+    } else {
+        return 1.f / (1.f + expf(-a));
+    }
 }
 
-// n of one group in place of x; returns r.  Lanes past the width hold zeros before and after.
+// n of one group in place of x; returns r.  inv: 1 / width.  Lanes past the width hold zeros before
+// and after.
 template <int VEC, int IT>
-__device__ __forceinline__ float normalise(float (&x)[IT][VEC], const bool (&on)[IT], int L, int width, float eps,
-                                           int center) {
-    const float inv = 1.f / static_cast<float>(width);
+__device__ __forceinline__ float normalise(float (&x)[IT][VEC], const bool (&on)[IT], int L, float inv, float eps,
+                                           bool center) {
     if (center) {
         float s = 0.f;
 #pragma unroll
@@ -104,7 +110,7 @@ __device__ __forceinline__ float normalise(float (&x)[IT][VEC], const bool (&on)
     for (int i = 0; i < IT; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) ss = fmaf(x[i][j], x[i][j], ss);
-    const float r = 1.f / sqrtf(lanes_sum(ss, L) * inv + eps);
+    const float r = rsqrtf(lanes_sum(ss, L) * inv + eps);
 #pragma unroll
     for (int i = 0; i < IT; ++i)
 #pragma unroll
@@ -114,35 +120,53 @@ __device__ __forceinline__ float normalise(float (&x)[IT][VEC], const bool (&on)
 
 constexpr int kThreads = 256;
 
-// Two groups to a group of lanes, half the grid apart in memory order (both in flight at once).
-template <typename E, int VEC, int IT>
-__global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int L, bool wide) {
+// What a call asks for: known at compile time (FLAGS = GATE + SILU + CENTER) for the widths that come
+// most, 16 bytes a lane in one vector; else (FLAGS < 0) tested as it runs.
+enum { GATE = 1, SILU = 2, CENTER = 4 };
+template <int FLAGS>
+struct Form {
+    bool gate, silu, center;
+    __device__ __forceinline__ explicit Form(const Args& a)
+        : gate(FLAGS < 0 ? a.gate != nullptr : (FLAGS & GATE) != 0),
+          silu(FLAGS < 0 ? a.silu != 0 : (FLAGS & SILU) != 0),
+          center(FLAGS < 0 ? a.center != 0 : (FLAGS & CENTER) != 0) {}
+};
+
+// Two groups to a group of lanes (2^lg lanes), both in flight at once.  I: the index type that holds
+// every group's number.
+template <typename E, int VEC, int IT, int FLAGS, typename I>
+__global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int lg, bool wide) {
     constexpr int U = IT * VEC <= 8 ? 2 : 1;
-    const int width = a.C / a.groups;
-    const long long total = a.rows * a.groups;
+    const Form<FLAGS> form(a);
+    const I groups = static_cast<I>(a.groups), total = static_cast<I>(a.rows) * groups;
+    const int width = a.width;
     const int lane = threadIdx.x & 31;
-    const int sub = lane / L, in = lane % L;
-    const int per = 32 / L;                                  // groups of lanes in a warp
-    const long long first = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (per * U) + sub;
+    const int L = 1 << lg, sub = lane >> lg, in = lane & (L - 1);
+    const int per = 32 >> lg;                                // groups of lanes in a warp
+    const I first = (static_cast<I>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (per * U) + sub;
+    int column = static_cast<int>(first % groups);           // the group's place in its row
     Pack<E, VEC> rx[U][IT], rt[U][IT];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const long long gi = first + u * per;
+            const I gi = first + u * per;
             const int e = (i * L + in) * VEC;
             if (gi < total && e < width) {
-                rx[u][i].load(static_cast<const E*>(a.x) + gi * width + e);
-                if (a.gate) rt[u][i].load(static_cast<const E*>(a.gate) + gi * width + e);
+                const long long at = static_cast<long long>(gi) * width + e;
+                rx[u][i].load(static_cast<const E*>(a.x) + at);
+                if (form.gate) rt[u][i].load(static_cast<const E*>(a.gate) + at);
             } else {
                 rx[u][i].clear();
             }
         }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const long long gi = first + u * per;
+        const I gi = first + u * per;
         const bool live = gi < total;                        // every lane takes part in the shuffles
-        const int wbase = static_cast<int>((live ? gi : 0) % a.groups) * width;
+        const int wbase = column * width;
+        column += a.advance;
+        if (column >= a.groups) column -= a.groups;
         float x[IT][VEC];
         bool on[IT];
 #pragma unroll
@@ -150,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int L, bo
             on[i] = live && (i * L + in) * VEC < width;
             rx[u][i].get(x[i]);
         }
-        normalise<VEC, IT>(x, on, L, width, a.eps, a.center);
+        normalise<VEC, IT>(x, on, L, a.inv, a.eps, form.center);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             if (!on[i]) continue;
@@ -158,27 +182,29 @@ __global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int L, bo
             float out[VEC], t[VEC], w[VEC], b[VEC];
             channel<VEC>(a.weight, wbase + e, wide, 1.f, w);
             channel<VEC>(a.bias, wbase + e, wide, 0.f, b);
-            if (a.gate) rt[u][i].get(t);
+            if (form.gate) rt[u][i].get(t);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const float z = fmaf(x[i][j], w[j], b[j]);
-                const float hot = a.gate ? t[j] : z;
-                const float act = a.silu ? hot * sigmoid<E>(hot) : hot;
-                out[j] = a.gate ? z * act : act;
+                const float hot = form.gate ? t[j] : z;
+                const float act = form.silu ? hot * sigmoid<E>(hot) : hot;
+                out[j] = form.gate ? z * act : act;
             }
-            store<E, VEC>(static_cast<E*>(a.y) + gi * width + e, out);
+            store<E, VEC>(static_cast<E*>(a.y) + static_cast<long long>(gi) * width + e, out);
         }
     }
 }
 
 // A group of lanes keeps one group column and walks the rows slot, slot + slots, ..., the next row on
-// its way while it works on one; its sums over those rows go to row `slot` of the partial sums.
-template <typename E, int VEC, int IT>
-__global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int L, int slots, bool wide) {
-    const int width = a.C / a.groups;
+// its way while it works on one; its sums over those rows go to row `slot` of the partial sums.  Lanes
+// and rows past the end hold zeros, which add nothing.
+template <typename E, int VEC, int IT, int FLAGS>
+__global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int lg, int slots, bool wide) {
+    const Form<FLAGS> form(a);
+    const int width = a.width;
     const int lane = threadIdx.x & 31;
-    const int sub = lane / L, in = lane % L;
-    const long long sw = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 / L) + sub;
+    const int L = 1 << lg, sub = lane >> lg, in = lane & (L - 1);
+    const long long sw = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 >> lg) + sub;
     const long long slot = sw / a.groups;
     const int wbase = static_cast<int>(sw % a.groups) * width;
     const bool mine = slot < slots;
@@ -193,18 +219,18 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
 #pragma unroll
         for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.f;
     }
-    const float inv = 1.f / static_cast<float>(width);
+    const float inv = a.inv;
     // every group of lanes of a warp makes the same number of rounds: shuffles need every lane
-    const long long rounds = (a.rows + slots - 1) / slots;
+    const int rounds = static_cast<int>((a.rows + slots - 1) / slots);
+    const long long step = static_cast<long long>(slots) * a.C;
     Pack<E, VEC> rx[IT], rd[IT], rt[IT];
-    const auto ask = [&](long long row) {
+    const auto ask = [&](long long row, long long at) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             if (on[i] && row < a.rows) {
-                const long long at = row * a.C + wbase + (i * L + in) * VEC;
-                rx[i].load(static_cast<const E*>(a.x) + at);
-                rd[i].load(static_cast<const E*>(a.dy) + at);
-                if (a.gate) rt[i].load(static_cast<const E*>(a.gate) + at);
+                rx[i].load(static_cast<const E*>(a.x) + at + i * L * VEC);
+                rd[i].load(static_cast<const E*>(a.dy) + at + i * L * VEC);
+                if (form.gate) rt[i].load(static_cast<const E*>(a.gate) + at + i * L * VEC);
             } else {
                 rx[i].clear();
                 rd[i].clear();
@@ -212,21 +238,19 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
             }
         }
     };
-    ask(slot);
-    for (long long n = 0; n < rounds; ++n) {
-        const long long row = n * slots + slot;
-        const long long base = row * a.C + wbase;
+    long long row = slot, at = slot * a.C + wbase + in * VEC;
+    ask(row, at);
+    for (int n = 0; n < rounds; ++n, row += slots, at += step) {
         float x[IT][VEC], t[IT][VEC], dz[IT][VEC];
-        bool here[IT];
+        const bool live = row < a.rows;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            here[i] = on[i] && row < a.rows;
             rx[i].get(x[i]);
             rd[i].get(dz[i]);
-            if (a.gate) rt[i].get(t[i]);
+            if (form.gate) rt[i].get(t[i]);
         }
-        ask(row + slots);
-        const float r = normalise<VEC, IT>(x, here, L, width, a.eps, a.center);
+        ask(row + slots, at + step);
+        const float r = normalise<VEC, IT>(x, on, L, a.inv, a.eps, form.center);
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -234,38 +258,39 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const float z = fmaf(x[i][j], w[i][j], bb[i][j]);
-                const float hot = a.gate ? t[i][j] : z;
+                const float hot = form.gate ? t[i][j] : z;
                 float act = hot, slope = 1.f;
-                if (a.silu) {
+                if (form.silu) {
                     const float s = sigmoid<E>(hot);
                     act = hot * s;
-                    slope = s * (1.f + hot * (1.f - s));
+                    slope = fmaf(act, 1.f - s, s);
                 }
-                if (a.gate) {
+                if (form.gate) {
                     dg[j] = dz[i][j] * z * slope;
                     dz[i][j] *= act;
                 } else {
                     dz[i][j] *= slope;
                 }
-                if (here[i]) {
-                    dw[i][j] = fmaf(dz[i][j], x[i][j], dw[i][j]);
-                    db[i][j] += dz[i][j];
-                }
-                dz[i][j] = here[i] ? dz[i][j] * w[i][j] : 0.f;
+                dw[i][j] = fmaf(dz[i][j], x[i][j], dw[i][j]);
+                db[i][j] += dz[i][j];
+                dz[i][j] *= w[i][j];
                 c1 = fmaf(dz[i][j], x[i][j], c1);
-                c2 += dz[i][j];
+                if (form.center) c2 += dz[i][j];
             }
-            if (a.gate && here[i]) store<E, VEC>(static_cast<E*>(a.dgate) + base + (i * L + in) * VEC, dg);
+            if (form.gate && live && on[i]) store<E, VEC>(static_cast<E*>(a.dgate) + at + i * L * VEC, dg);
         }
         c1 = lanes_sum(c1, L) * inv;
-        c2 = a.center ? lanes_sum(c2, L) * inv : 0.f;
+        if (form.center) c2 = lanes_sum(c2, L) * inv;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            if (!here[i]) continue;
+            if (!(live && on[i])) continue;
             float dx[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) dx[j] = r * (dz[i][j] - x[i][j] * c1 - c2);
-            store<E, VEC>(static_cast<E*>(a.dx) + base + (i * L + in) * VEC, dx);
+            for (int j = 0; j < VEC; ++j) {
+                const float d = fmaf(-x[i][j], c1, dz[i][j]);
+                dx[j] = r * (form.center ? d - c2 : d);
+            }
+            store<E, VEC>(static_cast<E*>(a.dx) + at + i * L * VEC, dx);
         }
     }
     if (!a.partial || !mine) return;
@@ -282,113 +307,132 @@ __global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int 
     }
 }
 
-// Column sums of the partial rows, in a fixed order: 32 columns a block, 8 threads a column.
-__global__ void __launch_bounds__(256) k_group_norm_columns(const float* partial, int slots, int C, float* dweight,
-                                                            float* dbias) {
-    __shared__ float s[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-    float* out = c < C ? dweight : dbias;
-    const int col = c < C ? c : c - C;
+// Column sums of the partial rows, in a fixed order: 32 columns a block, a warp to every 32nd row.
+__global__ void __launch_bounds__(1024) k_group_norm_columns(const float* partial, int slots, int C, float* dweight,
+                                                             float* dbias) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float sum = 0.f;
-    if (c < 2 * C && out)
-        for (int r = part; r < slots; r += 8) sum += partial[static_cast<long long>(r) * 2 * C + c];
-    s[part][threadIdx.x & 31] = sum;
-    __syncthreads();
-    if (part == 0 && c < 2 * C && out) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x & 31];
-        out[col] = t;
+    if (c < 2 * C) {
+#pragma unroll 8
+        for (int r = part; r < slots; r += 32) sum += partial[static_cast<long long>(r) * 2 * C + c];
     }
+    s[part][lane] = sum;
+    __syncthreads();
+    sum = s[lane][part];                     // column `part` of the block, its 32 sums over the lanes
+    sum = lanes_sum(sum, 32);
+    const int col = blockIdx.x * 32 + part;
+    float* out = col < C ? dweight : dbias;
+    if (lane == 0 && col < 2 * C && out) out[col < C ? col : col - C] = sum;
 }
 
-struct Shape { int vec, it, L; };
+struct Shape { int vec, it, lg; };
 
-// 16 bytes a lane where the width is a multiple of that, else 8 bytes, else single elements; the
+// 16 bytes a lane where the width is a multiple of that, else 8 bytes (bf16), else single elements; the
 // fewest lanes that hold the group with IT vectors each.
 Shape shape_of(bool is_bf16, int width) {
     const int full = is_bf16 ? 8 : 4;
     Shape s;
     s.vec = width % full == 0 ? full : (is_bf16 && width % 4 == 0 ? 4 : 1);
     const int n = (width + s.vec - 1) / s.vec;
-    s.it = n <= 32 ? 1 : (n <= 128 ? 4 : 16);
-    s.L = 1;
-    while (s.L < 32 && s.L * s.it < n) s.L *= 2;
+    s.it = n <= 32 && s.vec == full ? 1 : (n <= 128 ? 4 : 16);
+    s.lg = 0;
+    while (s.lg < 5 && (1 << s.lg) * s.it < n) ++s.lg;
     return s;
 }
-
 // weight and bias on 16 bytes (the C ABI asks for 4 only)
 bool wide_channels(const Args& a) {
     return ((reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
 }
+int flags_of(const Args& a) { return (a.gate ? GATE : 0) | (a.silu ? SILU : 0) | (a.center ? CENTER : 0); }
 
-template <typename E, int VEC, int IT>
-void run_forward(const Args& a, int L, cudaStream_t st) {
-    const long long per = (kThreads / 32) * (32 / L) * (IT * VEC <= 8 ? 2 : 1);
-    const long long blocks = (a.rows * a.groups + per - 1) / per;
-    k_group_norm<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L, wide_channels(a));
+// f.go<E, VEC, IT, FLAGS>() for a shape and a call's flags
+template <typename E, int VEC, typename F>
+void pick_form(int flags, F f) {
+    switch (flags) {
+    case 0: f.template go<E, VEC, 1, 0>(); break;
+    case 1: f.template go<E, VEC, 1, 1>(); break;
+    case 2: f.template go<E, VEC, 1, 2>(); break;
+    case 3: f.template go<E, VEC, 1, 3>(); break;
+    case 4: f.template go<E, VEC, 1, 4>(); break;
+    case 5: f.template go<E, VEC, 1, 5>(); break;
+    case 6: f.template go<E, VEC, 1, 6>(); break;
+    default: f.template go<E, VEC, 1, 7>(); break;
+    }
 }
-template <typename E, int VEC, int IT>
-void run_backward(const Args& a, int L, int slots, cudaStream_t st) {
-    const long long per = (kThreads / 32) * (32 / L);
-    const long long blocks = (static_cast<long long>(slots) * a.groups + per - 1) / per;
-    k_group_norm_grad<E, VEC, IT><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, L, slots, wide_channels(a));
-}
-
 template <typename F>
-void pick(bool is_bf16, const Shape& s, F f) {
+void pick(bool is_bf16, const Shape& s, int flags, F f) {
     if (is_bf16) {
-        if (s.vec == 8) { if (s.it == 1) f.template go<bf16, 8, 1>(); else f.template go<bf16, 8, 4>(); }
-        else if (s.vec == 4) { if (s.it == 1) f.template go<bf16, 4, 1>(); else f.template go<bf16, 4, 4>(); }
-        else if (s.it == 1) f.template go<bf16, 1, 1>();
-        else if (s.it == 4) f.template go<bf16, 1, 4>();
-        else f.template go<bf16, 1, 16>();
+        if (s.vec == 8) { if (s.it == 1) pick_form<bf16, 8>(flags, f); else f.template go<bf16, 8, 4, -1>(); }
+        else if (s.vec == 4) f.template go<bf16, 4, 4, -1>();
+        else if (s.it == 4) f.template go<bf16, 1, 4, -1>();
+        else f.template go<bf16, 1, 16, -1>();
     } else {
-        if (s.vec == 4) { if (s.it == 1) f.template go<float, 4, 1>(); else f.template go<float, 4, 4>(); }
-        else if (s.it == 1) f.template go<float, 1, 1>();
-        else if (s.it == 4) f.template go<float, 1, 4>();
-        else f.template go<float, 1, 16>();
+        if (s.vec == 4) { if (s.it == 1) pick_form<float, 4>(flags, f); else f.template go<float, 4, 4, -1>(); }
+        else if (s.it == 4) f.template go<float, 1, 4, -1>();
+        else f.template go<float, 1, 16, -1>();
     }
 }
 
 struct Forward {
     const Args& a;
-    int L;
+    int lg;
     cudaStream_t st;
-    template <typename E, int VEC, int IT> void go() { run_forward<E, VEC, IT>(a, L, st); }
+    template <typename E, int VEC, int IT, int FLAGS> void go() {
+        const long long per = (kThreads / 32) * (32 >> lg) * (IT * VEC <= 8 ? 2 : 1);
+        Args b = a;
+        b.advance = (32 >> lg) % a.groups;
+        const long long total = a.rows * a.groups;
+        const unsigned blocks = static_cast<unsigned>((total + per - 1) / per);
+        if (total + per < (1LL << 32)) k_group_norm<E, VEC, IT, FLAGS, unsigned><<<blocks, kThreads, 0, st>>>(b, lg, wide_channels(a));
+        else k_group_norm<E, VEC, IT, -1, unsigned long long><<<blocks, kThreads, 0, st>>>(b, lg, wide_channels(a));
+    }
 };
 struct Backward {
     const Args& a;
-    int L, slots;
+    int lg, slots;
     cudaStream_t st;
-    template <typename E, int VEC, int IT> void go() { run_backward<E, VEC, IT>(a, L, slots, st); }
+    template <typename E, int VEC, int IT, int FLAGS> void go() {
+        const long long per = (kThreads / 32) * (32 >> lg);
+        const long long blocks = (static_cast<long long>(slots) * a.groups + per - 1) / per;
+        k_group_norm_grad<E, VEC, IT, FLAGS><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a, lg, slots, wide_channels(a));
+    }
 };
 
 }  // namespace
 
-cudaError_t forward(const Args& a, bool is_bf16, cudaStream_t st) {
+static Args with_width(Args a) {
+    a.width = a.C / a.groups;
+    a.inv = 1.f / static_cast<float>(a.width);
+    return a;
+}
+
+cudaError_t forward(const Args& given, bool is_bf16, cudaStream_t st) {
+    const Args a = with_width(given);
     const Shape s = shape_of(is_bf16, a.C / a.groups);
-    pick(is_bf16, s, Forward{a, s.L, st});
+    pick(is_bf16, s, flags_of(a), Forward{a, s.lg, st});
     return cudaGetLastError();
 }
 
-// About four blocks an SM walk the rows (a partial row costs 8 C bytes twice), never more slots
+// About three blocks an SM walk the rows (a partial row costs 8 C bytes twice), never more slots
 // than rows.
 int partial_rows(bool is_bf16, long long rows, int C, int groups) {
     const Shape s = shape_of(is_bf16, C / groups);
-    const long long lanes = 148LL * 4 * kThreads;
-    long long slots = lanes / (static_cast<long long>(s.L) * groups);
+    const long long lanes = 148LL * 3 * kThreads;
+    long long slots = lanes / ((1LL << s.lg) * groups);
     if (slots < 1) slots = 1;
     return static_cast<int>(slots < rows ? slots : rows);
 }
 
-cudaError_t backward(const Args& a, bool is_bf16, cudaStream_t st) {
+cudaError_t backward(const Args& given, bool is_bf16, cudaStream_t st) {
+    const Args a = with_width(given);
     const Shape s = shape_of(is_bf16, a.C / a.groups);
     const int slots = partial_rows(is_bf16, a.rows, a.C, a.groups);
-    pick(is_bf16, s, Backward{a, s.L, slots, st});
+    pick(is_bf16, s, flags_of(a), Backward{a, s.lg, slots, st});
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
-    k_group_norm_columns<<<(2 * a.C + 31) / 32, 256, 0, st>>>(a.partial, slots, a.C, a.dweight, a.dbias);
+    k_group_norm_columns<<<(2 * a.C + 31) / 32, 1024, 0, st>>>(a.partial, slots, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 
