@@ -23,16 +23,31 @@ struct Problem {
 
 // Chunk by chunk on the tensor cores (delta_forward.cu), with forward_bytes() of workspace.
 size_t forward_bytes(const Problem& p);
+int forward_launches(const Problem& p);
 cudaError_t forward(const Problem& p, void* ws, cudaStream_t st);
 
 // The chunks' records (delta_prepare.cu); gradients: the form that the backward pass reads.
 size_t records_bytes(const Problem& p, bool gradients);
 cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st);
 
+// How a sequence is cut (delta_fold.cu): `count` segments of `chunks` chunks (1: not at all), and the
+// floats of the segments' summaries and of the states before them.
+struct Segments {
+    int count, chunks;
+    size_t sums, starts;
+};
+Segments segments(const Problem& p);
+// The states between the segments, from the first on: sums [BH][count - 1][d][dv | d] holds (B | A) of
+// every segment but the last (the first one's B from the given state), first the given state or null.
+// With back: from the last on, S = A^T S' + back [BH][count][d][dv].  out: [BH][count][d][dv].
+cudaError_t fold(const Problem& p, const Segments& g, const float* sums, const float* back, const float* first,
+                 float* out, cudaStream_t st);
+
 // The forward walk for the gradients: the state before each block of block_chunks chunks
-// [BH][blocks][d][dv] and each token's error R [BH][T][dv]; records in the gradients' form.
-cudaError_t store_states(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
-                         cudaStream_t st);
+// [BH][blocks][d][dv] and each token's error R [BH][T][dv]; records in the gradients' form.  sums and
+// starts: segments(p)'s floats (sums is read again for the reverse walk).
+cudaError_t store_states(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states,
+                         float* errors, int block_chunks, cudaStream_t st);
 
 // Gradients (delta_backward.cu).  dstate_out: the gradient at the last state, or null; dstate_in: the
 // one at the first state, or null when it is not wanted.

@@ -56,7 +56,8 @@ size_t hla_delta_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T,
 }
 
 int hla_delta_kernel_launches(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
-    return check_shape(dtype, B, Hk, H, T, d, dv) == HLA_OK ? 2 : 0;
+    if (check_shape(dtype, B, Hk, H, T, d, dv) != HLA_OK) return 0;
+    return hla::delta::forward_launches(sizes(dtype, B, Hk, H, T, d, dv));
 }
 
 hla_status_t hla_delta_forward(const void* q, const void* k, const void* v, const float* g, const float* beta,

@@ -22,17 +22,22 @@ namespace {
 struct ReverseArgs {
     const void *q, *k, *dout;
     const uint8_t* records;   // gradients' form
-    const float* dstate_out;  // [BH][d][dv] or null
+    const float* behind;      // dS behind each segment [BH][segments][d][dv]; SUMMARY: behind the last one
+                              // [BH][d][dv]; or null
     const int* lengths;
     float* dstate_in;         // [BH][d][dv] or null
     float* dstates;           // [BH][blocks][d][dv]: dS behind each block
     float* H;                 // [BH][T][dv]
+    float* back;              // SUMMARY: [BH][segments][d][dv], dS before each segment from zero behind it
     int Hk, Hv, T, dv, bthd, block_chunks;
+    int segments, seg_chunks;
     float scale;
 };
 
-template <typename E, int DK_, int NG_>
+// SUMMARY: only dS before each segment but the first, from zero (behind the last: from what is given).
+template <typename E, int DK_, int NG_, bool SUMMARY_>
 struct Rev {
+    static constexpr bool SUMMARY = SUMMARY_;
     using Elem = E;
     static constexpr int DK = DK_, CS = 16 * NG_;
     static constexpr bool BF = sizeof(E) == 2;
@@ -57,10 +62,14 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slices = a.dv / CS, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * CS;
+    const int slices = a.dv / CS, walked = F::SUMMARY ? a.segments - 1 : a.segments;
+    const int col0 = (blockIdx.x % slices) * CS, bh = blockIdx.x / slices / walked;
+    const int seg = (blockIdx.x / slices) % walked + (F::SUMMARY ? 1 : 0);
     const int b = bh / a.Hv, h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
     const int T = length_of(a.lengths, b, a.T);
-    const int all_chunks = (a.T + C - 1) / C, chunks = (T + C - 1) / C;
+    const int all_chunks = (a.T + C - 1) / C, live_chunks = (T + C - 1) / C;
+    const int c_first = seg * a.seg_chunks, c_end = min(live_chunks, c_first + a.seg_chunks);
+    const int chunks = max(0, c_end - c_first);
     const int blocks = (all_chunks + a.block_chunks - 1) / a.block_chunks;
     const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.Hv);
     constexpr int w_load = F::W_STATE;
@@ -69,7 +78,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
     float S[DH / 8][4];                                 // dS^T, as the forward walk holds S^T
     const int own_col = col0 + 16 * grp + (lane >> 2), own_key = part * DH + 2 * (lane & 3);
     if (warp < w_load) {
-        const float* from = a.dstate_out ? a.dstate_out + static_cast<long long>(bh) * DK * a.dv : nullptr;
+        const float* from = nullptr;
+        if (a.behind && !F::SUMMARY) from = a.behind + (static_cast<long long>(bh) * a.segments + seg) * DK * a.dv;
+        if (a.behind && F::SUMMARY && seg == a.segments - 1) from = a.behind + static_cast<long long>(bh) * DK * a.dv;
 #pragma unroll
         for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
@@ -88,10 +99,10 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
         uint8_t* const vf = reinterpret_cast<uint8_t*>(ex - lane);
         int stage = 0;
         for (int s = -F::AHEAD; s < 0; ++s) step_end();
-        for (int c = chunks - 1; c >= 0; --c) {
+        for (int c = c_end - 1; c >= c_first; --c) {
             const uint32_t so = stage * F::STAGE;
             const Gates* G = reinterpret_cast<const Gates*>(sm + stage * F::STAGE + F::gates);
-            if (c % a.block_chunks == a.block_chunks - 1 || c == chunks - 1) {
+            if (!F::SUMMARY && (c % a.block_chunks == a.block_chunks - 1 || c == live_chunks - 1)) {
                 float* to = a.dstates + (static_cast<long long>(bh) * blocks + c / a.block_chunks) * DK * a.dv +
                             static_cast<long long>(own_key) * a.dv + own_col;
 #pragma unroll
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
                 float* to = a.H + (static_cast<long long>(bh) * a.T + tok) * a.dv + own_col;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (tok + (j & 1) < T) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[j];
+                    if (!F::SUMMARY && tok + (j & 1) < T) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[j];
                 const float f0 = -since[e].x * beta[e].x, f1 = -since[e].y * beta[e].y;
                 uint32_t t0[3], t1[3];
                 split<3>(u[0] * f0, u[1] * f1, t0);
@@ -284,8 +295,8 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
         const uint8_t* rec = a.records + static_cast<long long>(bh) * all_chunks * REC;
         int stage = 0;
         for (int i = 0; i < chunks + F::AHEAD; ++i) {
-            const int c = chunks - 1 - i;
-            if (c >= 0) {
+            const int c = c_end - 1 - i;
+            if (c >= c_first) {
                 const uint32_t sg = sb + stage * F::STAGE;
                 const int rows = min(C, T - c * C);
                 const uint8_t* from = rec + static_cast<long long>(c) * REC + kXBytes;
@@ -301,8 +312,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
             step_end();
         }
     }
-    if (warp < w_load && a.dstate_in) {
-        float* to = a.dstate_in + static_cast<long long>(bh) * DK * a.dv;
+    float* const to = F::SUMMARY ? a.back + (static_cast<long long>(bh) * a.segments + seg) * DK * a.dv
+                                 : (a.dstate_in && seg == 0 ? a.dstate_in + static_cast<long long>(bh) * DK * a.dv : nullptr);
+    if (warp < w_load && to) {
 #pragma unroll
         for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(256) k_delta_share(const float* dq, const floa
 int block_tokens(const Problem& p) { return !p.bf16 && (p.d == 128 || p.dv == 128) ? 32 : 64; }
 
 struct Space {   // the workspace's pieces, bytes from its start
-    size_t records, states, dstates, R, H, dq, dk, end;
+    size_t records, states, dstates, R, H, dq, dk, sums, starts, back, behind, end;
 };
 Space space(const Problem& p) {
     const size_t BH = static_cast<size_t>(p.B) * p.H, blocks = (p.T + block_tokens(p) - 1) / block_tokens(p);
@@ -874,20 +886,43 @@ Space space(const Problem& p) {
     s.H = s.R + rows;
     s.dq = s.H + rows;
     s.dk = s.dq + part;
-    s.end = s.dk + part;
+    const Segments g = segments(p);
+    s.sums = s.dk + part;
+    s.starts = s.sums + g.sums * 4;
+    s.back = s.starts + g.starts * 4;
+    s.behind = s.back + g.starts * 4;
+    s.end = s.behind + g.starts * 4;
     return s;
 }
 
-template <typename E, int DK>
-cudaError_t reverse(const Problem& p, const Gradients& gr, const uint8_t* records, float* dstates, float* H, cudaStream_t st) {
-    using F = Rev<E, DK, sizeof(E) == 2 ? 2 : 1>;
+template <typename F>
+cudaError_t start(const ReverseArgs& a, int blocks, cudaStream_t st) {
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
-    const ReverseArgs a{p.q, p.k, gr.dout, records, gr.dstate_out, p.lengths, gr.dstate_in, dstates, H,
-                        p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, block_tokens(p) / C, p.scale};
-    cudaError_t e = cudaFuncSetAttribute(k_delta_reverse<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_reverse<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
     if (e != cudaSuccess) return e;
-    k_delta_reverse<F><<<p.B * p.H * (p.dv / F::CS), F::WARPS * 32, F::bytes, st>>>(a);
+    k_delta_reverse<F><<<blocks, F::WARPS * 32, F::bytes, st>>>(a);
     return cudaGetLastError();
+}
+
+// The reverse walk; over segments with what lies behind each from a summary of the later ones (the
+// linear part of a segment backwards is the transpose of the forward walk's A).
+template <typename E, int DK>
+cudaError_t reverse(const Problem& p, const Gradients& gr, char* ws, const Space& s, cudaStream_t st) {
+    constexpr int NG = sizeof(E) == 2 ? 2 : 1;
+    const Segments g = segments(p);
+    const int slices = p.dv / (16 * NG), BH = p.B * p.H;
+    float* back = reinterpret_cast<float*>(ws + s.back);
+    float* behind = reinterpret_cast<float*>(ws + s.behind);
+    ReverseArgs a{p.q, p.k, gr.dout, reinterpret_cast<uint8_t*>(ws + s.records), gr.dstate_out, p.lengths, gr.dstate_in,
+                  reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.H), back,
+                  p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, block_tokens(p) / C, g.count, g.chunks, p.scale};
+    if (g.count > 1) {
+        cudaError_t e = start<Rev<E, DK, NG, true>>(a, BH * (g.count - 1) * slices, st);
+        if (e == cudaSuccess) e = fold(p, g, reinterpret_cast<float*>(ws + s.sums), back, gr.dstate_out, behind, st);
+        if (e != cudaSuccess) return e;
+        a.behind = behind;
+    }
+    return start<Rev<E, DK, NG, false>>(a, BH * g.count * slices, st);
 }
 
 template <typename E, int DK, int DV>
@@ -915,10 +950,9 @@ cudaError_t all(const Problem& p, const Gradients& gr, char* ws, cudaStream_t st
     uint8_t* records = reinterpret_cast<uint8_t*>(ws + s.records);
     cudaError_t e = prepare(p, true, records, st);
     if (e == cudaSuccess)
-        e = store_states(p, records, reinterpret_cast<float*>(ws + s.states), reinterpret_cast<float*>(ws + s.R),
-                         block_tokens(p) / C, st);
-    if (e == cudaSuccess)
-        e = reverse<E, DK>(p, gr, records, reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.H), st);
+        e = store_states(p, records, reinterpret_cast<float*>(ws + s.sums), reinterpret_cast<float*>(ws + s.starts),
+                         reinterpret_cast<float*>(ws + s.states), reinterpret_cast<float*>(ws + s.R), block_tokens(p) / C, st);
+    if (e == cudaSuccess) e = reverse<E, DK>(p, gr, ws, s, st);
     if (e == cudaSuccess) {
         if (p.dv == 32) e = block_grads<E, DK, 32>(p, gr, ws, s, st);
         else if (p.dv == 64) e = block_grads<E, DK, 64>(p, gr, ws, s, st);
@@ -938,7 +972,7 @@ cudaError_t all(const Problem& p, const Gradients& gr, char* ws, cudaStream_t st
 }  // namespace
 
 size_t backward_bytes(const Problem& p) { return space(p).end; }
-int backward_launches(const Problem& p) { return p.H != p.Hk ? 5 : 4; }
+int backward_launches(const Problem& p) { return (p.H != p.Hk ? 5 : 4) + (segments(p).count > 1 ? 4 : 0); }
 
 cudaError_t backward(const Problem& p, const Gradients& gr, void* ws, cudaStream_t st) {
     char* w = static_cast<char*>(ws);

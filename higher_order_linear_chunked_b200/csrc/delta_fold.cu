@@ -1,0 +1,120 @@
+// Segments of long sequences: how many, and the states between them.
+#include "delta_walk.cuh"
+
+namespace hla {
+namespace delta {
+namespace {
+
+struct FoldArgs {
+    const float *sums, *back, *first;
+    float* out;
+    int dv, count;
+};
+
+// S <- A S + B from segment to segment (REV: S <- A^T S + G, from the last to the first), 16 columns of
+// one head a block; a thread has four columns of one row, the next segment's A is on its way meanwhile.
+// fp32 on the CUDA cores: a segment costs 2 d d 16 flops a block, a small part of a walk over it.
+template <int DK, bool REV>
+__global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
+    constexpr int NT = DK * 4, LD = DK + 1, U = DK * DK / 4 / NT;      // float4 of A a thread
+    extern __shared__ __align__(16) float sm[];
+    float* As = sm;                                                    // [k][row]
+    float4* Ss = reinterpret_cast<float4*>(sm + (DK * LD + 3) / 4 * 4);   // [k][4 x 4 columns]
+    const int slices = a.dv / 16, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * 16;
+    const int tid = threadIdx.x, r = tid % DK, cg = tid / DK, width = a.dv + DK;
+    const int N = a.count;
+    const auto A = [&](int s) { return a.sums + (static_cast<long long>(bh) * (N - 1) + s) * DK * width + a.dv; };
+    const auto add = [&](int s) {
+        return REV ? a.back + ((static_cast<long long>(bh) * N + s) * DK + r) * a.dv + col0 + 4 * cg
+                   : a.sums + ((static_cast<long long>(bh) * (N - 1) + s) * DK + r) * width + col0 + 4 * cg;
+    };
+    const auto put = [&](int s, const float (&x)[4]) {
+        store4(a.out + ((static_cast<long long>(bh) * N + s) * DK + r) * a.dv + col0 + 4 * cg, x);
+    };
+    const int step = REV ? -1 : 1, s0 = REV ? N - 1 : 0, last = REV ? 0 : N - 1;
+    float cur[4] = {};
+    if (a.first) load4(a.first + (static_cast<long long>(bh) * DK + r) * a.dv + col0 + 4 * cg, cur);
+    put(s0, cur);
+    load4(add(s0), cur);
+    put(s0 + step, cur);
+    float4 next[U];
+    const auto ask = [&](int s) {
+        if (s == last) return;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = tid + u * NT;
+            next[u] = *reinterpret_cast<const float4*>(A(s) + (i / (DK / 4)) * width + (i % (DK / 4)) * 4);
+        }
+    };
+    ask(s0 + step);
+    for (int s = s0 + step; s != last; s += step) {
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = tid + u * NT, row = i / (DK / 4), c = (i % (DK / 4)) * 4;
+            const float x[4] = {next[u].x, next[u].y, next[u].z, next[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) As[REV ? row * LD + c + j : (c + j) * LD + row] = x[j];
+        }
+        Ss[r * 4 + cg] = make_float4(cur[0], cur[1], cur[2], cur[3]);
+        __syncthreads();
+        ask(s + step);
+        load4(add(s), cur);
+#pragma unroll 16
+        for (int k = 0; k < DK; ++k) {
+            const float x = As[k * LD + r];
+            const float4 y = Ss[k * 4 + cg];
+            cur[0] = fmaf(x, y.x, cur[0]);
+            cur[1] = fmaf(x, y.y, cur[1]);
+            cur[2] = fmaf(x, y.z, cur[2]);
+            cur[3] = fmaf(x, y.w, cur[3]);
+        }
+        put(s + step, cur);
+    }
+}
+
+template <int DK, bool REV>
+cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
+    constexpr int bytes = ((DK * (DK + 1) + 3) / 4 * 4 + DK * 16) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_fold<DK, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 16), DK * 4, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
+// as often as the heads' column slices fill the SMs; with them, the summaries' walk (no outputs: about
+// 0.8 of a step), the fold (0.4 a segment) and the second walk.  Taken when a tenth is gained.
+Segments segments(const Problem& p) {
+    constexpr int SMS = 148;
+    const long long BH = static_cast<long long>(p.B) * p.H;
+    const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16;
+    const auto waves = [](long long blocks) { return static_cast<double>((blocks + SMS - 1) / SMS); };
+    int best = 1;
+    double cost = 0.9 * waves(BH * p.dv / CS) * NC;
+    for (int n = 2; n <= 64 && n <= NC / 4; ++n) {
+        const int chunks = (NC + n - 1) / n;
+        if ((NC + chunks - 1) / chunks != n) continue;
+        const double c = 0.8 * chunks * waves(BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS) + 0.4 * n + 8 +
+                         chunks * waves(BH * n * p.dv / CS);
+        if (c < cost) cost = c, best = n;
+    }
+    Segments g{best, (NC + best - 1) / best, 0, 0};
+    if (best > 1) {
+        g.sums = static_cast<size_t>(BH) * (best - 1) * p.d * (p.dv + p.d);
+        g.starts = static_cast<size_t>(BH) * best * p.d * p.dv;
+    }
+    return g;
+}
+
+cudaError_t fold(const Problem& p, const Segments& g, const float* sums, const float* back, const float* first,
+                 float* out, cudaStream_t st) {
+    const FoldArgs a{sums, back, first, out, p.dv, g.count};
+    if (back) return p.d == 32 ? run<32, true>(p, a, st) : p.d == 64 ? run<64, true>(p, a, st) : run<128, true>(p, a, st);
+    return p.d == 32 ? run<32, false>(p, a, st) : p.d == 64 ? run<64, false>(p, a, st) : run<128, false>(p, a, st);
+}
+
+}  // namespace delta
+}  // namespace hla

@@ -9,6 +9,11 @@
 // A block owns CS = 16 NG value columns of one head (S's columns do not mix).  NH warps hold the
 // state of 16 columns transposed in registers, each a part of the key axis; between the products
 // they share the chunk's Y and U, each splitting the tokens of its part once, through shared memory.
+//
+// One head's chunks follow one another, so few long heads leave most of the machine idle.  Then the
+// sequence is cut into segments (delta_fold.cu): a first walk takes each segment from a zero state and
+// also takes the unit matrix through it without values, which gives S_end = A S_start + B; the states
+// between the segments follow from those, and the second walk has all segments at once.
 #include "delta_walk.cuh"
 
 namespace hla {
@@ -33,7 +38,8 @@ struct WalkArgs {
     float scale;
 };
 
-template <typename E, int DK_, int NG_, Mode MODE_>
+// GR: the records have the gradients' form.
+template <typename E, int DK_, int NG_, Mode MODE_, bool GR>
 struct Cfg {
     using Elem = E;
     static constexpr int DK = DK_, NG = NG_, CS = 16 * NG_;
@@ -42,7 +48,7 @@ struct Cfg {
     static constexpr int KT = BF ? 1 : 3;             // terms of q, k
     static constexpr int OT = BF ? 2 : 3;             // terms of S0, U and P in the outputs: twice the
                                                       // 8 bits that a bf16 output keeps
-    static constexpr int INV = MODE_ == STORE ? 2 : 1, PT = MODE_ == STORE ? 3 : OT;   // the records' form
+    static constexpr int INV = GR ? 2 : 1, PT = GR ? 3 : OT;
     static constexpr int AHEAD = BF ? 3 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
     static constexpr int NH = DK_ == 128 ? 4 : 2;     // state warps of 16 columns
@@ -432,47 +438,72 @@ cudaError_t start(const WalkArgs& a, int blocks, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename E, int DK>
-cudaError_t walk(const Problem& p, void* ws, cudaStream_t st) {
-    constexpr int NG = sizeof(E) == 2 ? 2 : 1;
-    using F = Cfg<E, DK, NG, OUT>;
+// The states before the segments: the segments' summaries, then one after another.
+template <typename E, int DK, bool GR>
+cudaError_t states_between(const Problem& p, const Segments& g, const uint8_t* records, float* sums, float* starts,
+                           cudaStream_t st) {
+    using F = Cfg<E, DK, sizeof(E) == 2 ? 2 : 1, SUMMARY, GR>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
-    const int BH = p.B * p.H, NC = (p.T + C - 1) / C;
-    uint8_t* records = static_cast<uint8_t*>(ws);
-    cudaError_t e = prepare(p, false, records, st);
-    if (e != cudaSuccess) return e;
-    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, p.o, p.state_out, nullptr, nullptr, nullptr, 1,
-               p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, 1, NC, p.scale};
-    return start<F>(a, BH * (p.dv / F::CS), st);
+    const WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, nullptr, nullptr, sums, nullptr, nullptr, 1,
+                     p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
+    const cudaError_t e = start<F>(a, p.B * p.H * (g.count - 1) * ((p.dv + DK) / F::CS), st);
+    return e == cudaSuccess ? fold(p, g, sums, nullptr, p.state_in, starts, st) : e;
 }
 
 template <typename E, int DK>
-cudaError_t walk_store(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
-                       cudaStream_t st) {
+cudaError_t walk(const Problem& p, void* ws, cudaStream_t st) {
     constexpr int NG = sizeof(E) == 2 ? 2 : 1;
-    using F = Cfg<E, DK, NG, STORE>;
+    using F = Cfg<E, DK, NG, OUT, false>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
-    const int BH = p.B * p.H, NC = (p.T + C - 1) / C;
-    WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, nullptr, nullptr, nullptr, states, errors, block_chunks,
-               p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, 1, NC, p.scale};
-    return start<F>(a, BH * (p.dv / F::CS), st);
+    const int BH = p.B * p.H;
+    char* w = static_cast<char*>(ws);
+    uint8_t* records = reinterpret_cast<uint8_t*>(w);
+    const Segments g = segments(p);
+    float* sums = reinterpret_cast<float*>(w + records_bytes(p, false));
+    float* starts = sums + g.sums;
+    cudaError_t e = prepare(p, false, records, st);
+    if (e == cudaSuccess && g.count > 1) e = states_between<E, DK, false>(p, g, records, sums, starts, st);
+    if (e != cudaSuccess) return e;
+    WalkArgs a{p.q, p.k, p.v, records, g.count > 1 ? starts : p.state_in, p.lengths, p.o, p.state_out, nullptr, nullptr,
+               nullptr, 1, p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
+    return start<F>(a, BH * g.count * (p.dv / F::CS), st);
+}
+
+template <typename E, int DK>
+cudaError_t walk_store(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states, float* errors,
+                       int block_chunks, cudaStream_t st) {
+    constexpr int NG = sizeof(E) == 2 ? 2 : 1;
+    using F = Cfg<E, DK, NG, STORE, true>;
+    static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
+    const Segments g = segments(p);
+    if (g.count > 1) {
+        const cudaError_t e = states_between<E, DK, true>(p, g, records, sums, starts, st);
+        if (e != cudaSuccess) return e;
+    }
+    WalkArgs a{p.q, p.k, p.v, records, g.count > 1 ? starts : p.state_in, p.lengths, nullptr, nullptr, nullptr, states,
+               errors, block_chunks, p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
+    return start<F>(a, p.B * p.H * g.count * (p.dv / F::CS), st);
 }
 
 }  // namespace
 
-cudaError_t store_states(const Problem& p, const uint8_t* records, float* states, float* errors, int block_chunks,
-                         cudaStream_t st) {
+cudaError_t store_states(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states,
+                         float* errors, int block_chunks, cudaStream_t st) {
     if (p.bf16) {
-        if (p.d == 32) return walk_store<bf16, 32>(p, records, states, errors, block_chunks, st);
-        if (p.d == 64) return walk_store<bf16, 64>(p, records, states, errors, block_chunks, st);
-        return walk_store<bf16, 128>(p, records, states, errors, block_chunks, st);
+        if (p.d == 32) return walk_store<bf16, 32>(p, records, sums, starts, states, errors, block_chunks, st);
+        if (p.d == 64) return walk_store<bf16, 64>(p, records, sums, starts, states, errors, block_chunks, st);
+        return walk_store<bf16, 128>(p, records, sums, starts, states, errors, block_chunks, st);
     }
-    if (p.d == 32) return walk_store<float, 32>(p, records, states, errors, block_chunks, st);
-    if (p.d == 64) return walk_store<float, 64>(p, records, states, errors, block_chunks, st);
-    return walk_store<float, 128>(p, records, states, errors, block_chunks, st);
+    if (p.d == 32) return walk_store<float, 32>(p, records, sums, starts, states, errors, block_chunks, st);
+    if (p.d == 64) return walk_store<float, 64>(p, records, sums, starts, states, errors, block_chunks, st);
+    return walk_store<float, 128>(p, records, sums, starts, states, errors, block_chunks, st);
 }
 
-size_t forward_bytes(const Problem& p) { return records_bytes(p, false); }
+size_t forward_bytes(const Problem& p) {
+    const Segments g = segments(p);
+    return records_bytes(p, false) + sizeof(float) * (g.sums + g.starts);
+}
+int forward_launches(const Problem& p) { return segments(p).count > 1 ? 4 : 2; }
 
 cudaError_t forward(const Problem& p, void* ws, cudaStream_t st) {
     if (p.bf16) {

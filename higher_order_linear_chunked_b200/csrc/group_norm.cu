@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int lg, b
 // its way while it works on one; its sums over those rows go to row `slot` of the partial sums.  Lanes
 // and rows past the end hold zeros, which add nothing.
 template <typename E, int VEC, int IT, int FLAGS>
-__global__ void __launch_bounds__(kThreads) k_group_norm_grad(const Args a, int lg, int slots, bool wide) {
+__global__ void __launch_bounds__(kThreads, IT == 1 ? 3 : 1) k_group_norm_grad(const Args a, int lg, int slots, bool wide) {
     const Form<FLAGS> form(a);
     const int width = a.width;
     const int lane = threadIdx.x & 31;

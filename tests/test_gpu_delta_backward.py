@@ -131,6 +131,19 @@ def test_long_and_many(dtype):
     compare(*inputs(dtype, 20, 2, 4, 70, 32, 64, seed=13), 0.2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,dv", [(32, 64), (64, 64), (128, 128)])
+def test_segments_of_a_padded_batch(dtype, d, dv):
+    """Few heads and many tokens: both walks go in segments, some of them behind an end."""
+    lens = torch.tensor([1000, 330, 0], dtype=torch.int32)
+    x, dout, dstate = inputs(dtype, 3, 1, 1, 1000, d, dv, seed=15, slow=4.0)
+    assert hla.delta._library().hla_delta_backward_kernel_launches(1 if dtype == "bf16" else 0, 3, 1, 1, 1000, d, dv) == 8
+    for b, n in enumerate(lens.tolist()):
+        for t in (*x[:5], dout):
+            t[b, :, n:] = 0.0
+    compare(x, dout, dstate, 0.2, lens)
+
+
 def test_against_differences():
     """fp32: the slope of the GPU forward along a direction, by a central difference.  The loss's own
     rounding (2^-24 of its terms' sizes, about 1e-6 of the loss's scale) over the step of 1e-2, and the
