@@ -85,19 +85,23 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
-// as often as the heads' column slices fill the SMs; with them, the summaries' walk (no outputs: about
-// 0.8 of a step), the fold (0.4 a segment) and the second walk.  Taken when a tenth is gained.
+// as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
+// takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step), the
+// fold (0.4 a segment) and the second walk.  Taken when a tenth is gained.
 Segments segments(const Problem& p) {
     constexpr int SMS = 148;
     const long long BH = static_cast<long long>(p.B) * p.H;
-    const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16;
-    const auto waves = [](long long blocks) { return static_cast<double>((blocks + SMS - 1) / SMS); };
+    const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16, fit = p.bf16 ? (p.d <= 64 ? 2 : 1) : (p.d == 32 ? 2 : 1);
+    const auto waves = [&](long long blocks) {
+        const long long rest = blocks % (SMS * fit);
+        return (fit == 2 ? 1.25 : 1.0) * static_cast<double>(blocks / (SMS * fit)) + (rest == 0 ? 0.0 : rest <= SMS ? 1.0 : 1.25);
+    };
     int best = 1;
     double cost = 0.9 * waves(BH * p.dv / CS) * NC;
     for (int n = 2; n <= 64 && n <= NC / 4; ++n) {
         const int chunks = (NC + n - 1) / n;
         if ((NC + chunks - 1) / chunks != n) continue;
-        const double c = 0.8 * chunks * waves(BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS) + 0.4 * n + 8 +
+        const double c = 0.85 * chunks * waves(BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS) + 0.4 * n + 8 +
                          chunks * waves(BH * n * p.dv / CS);
         if (c < cost) cost = c, best = n;
     }

@@ -42,16 +42,19 @@ struct WalkArgs {
 template <typename E, int DK_, int NG_, Mode MODE_, bool GR>
 struct Cfg {
     using Elem = E;
-    static constexpr int DK = DK_, NG = NG_, CS = 16 * NG_;
+    static constexpr int DK = DK_, CS = 16 * NG_;
     static constexpr Mode MODE = MODE_;
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;             // terms of q, k
     static constexpr int OT = BF ? 2 : 3;             // terms of S0, U and P in the outputs: twice the
                                                       // 8 bits that a bf16 output keeps
     static constexpr int INV = GR ? 2 : 1, PT = GR ? 3 : OT;
-    static constexpr int AHEAD = BF ? 3 : 1;          // chunks between a tile's request and its use
+    static constexpr int AHEAD = BF ? 2 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
-    static constexpr int NH = DK_ == 128 ? 4 : 2;     // state warps of 16 columns
+    // state warps of 16 columns: one holds 64 keys' part of the state and the chunk's terms in its
+    // registers (bf16: 4x16x4096x64 the same with one and two, with half the warps); more keys, or the
+    // six products of fp32 terms, are worth the exchanges
+    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2);
     static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? NG_ : 0;
     static constexpr int WARPS = W_STATE + W_OUT + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2;
@@ -71,15 +74,16 @@ struct Cfg {
     static constexpr int uf = sf + (MODE_ == OUT ? 2 * SB : 0);
     static constexpr int UB = NG_ * 2 * OT * 512;
     static constexpr int ex = uf + (MODE_ == OUT ? 2 * UB : 0);
-    static constexpr int yf = ex + W_STATE * 2048;    // Y of the chunk as an A operand; the decayed U
+    static constexpr int yf = ex + (NH > 1 ? W_STATE * 2048 : 0);    // Y of the chunk as an A operand; the decayed U
     static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
-    static constexpr int bytes = yf + NG_ * YB;
+    static constexpr int bytes = yf + (NH > 1 ? NG_ * YB : 0);
+    static constexpr int BLOCKS = bytes <= 113 * 1024 ? 2 : 1;   // of an SM
 };
 
 template <typename F>
-__global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs a) {
+__global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const WalkArgs a) {
     using E = typename F::Elem;
-    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, CS = F::CS, KT = F::KT, OT = F::OT;
+    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / (NH == 1 ? 2 : NH), CS = F::CS, KT = F::KT, OT = F::OT;
     constexpr Mode MODE = F::MODE;
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzles are exclusive ors of address bits
     const uint32_t sb = ptx::smem_u32(sm);
@@ -153,6 +157,99 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
                         for (int j = 0; j < 4; ++j) to[static_cast<long long>(8 * n + (j & 1)) * a.dv + 8 * (j >> 1)] = S[n][j];
                 }
             }
+            if constexpr (NH == 1) {
+                // one warp has the whole key axis: everything stays in its registers
+                float y[4][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    uint32_t bk[2][KT][4], as[3][4];
+#pragma unroll
+                    for (int np = 0; np < 2; ++np)
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)   // a step of 16 keys changes the piece by two: its swizzle is an exclusive or
+                            ldsm4(bk[np][t], ((k_n + so) ^ (ks << 5)) + t * (C * DK * 2) + np * 16 * DK * 2);
+                    split_a<3>(S[2 * ks], S[2 * ks + 1], as);
+                    prod<3, KT, 2>(y, as, bk);
+                    if (MODE == OUT) {
+#pragma unroll
+                        for (int t = 0; t < OT; ++t) sf[(ks * OT + t) * 32] = make_uint4(as[t][0], as[t][1], as[t][2], as[t][3]);
+                    }
+                }
+                // Y^T = V^T - (S0^T K^T) e^c
+                float v[4][4] = {};
+                if (!unit) {
+                    cols_t<CS>(static_cast<const E*>(nullptr), sb + F::v + so, 16 * grp, 0, lane, v[0], v[1]);
+                    cols_t<CS>(static_cast<const E*>(nullptr), sb + F::v + so, 16 * grp, 16, lane, v[2], v[3]);
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 f = *reinterpret_cast<const float2*>(&G->since[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[n][j] = fmaf((j & 1) ? -f.y : -f.x, y[n][j], v[n][j]);
+                }
+                // R^T = Y^T X^T; X is lower triangular
+                const uint32_t x_n = at_pieces_first<C * 2>(sb + F::x + so, 0, 0, lane);
+                float r[4][4] = {};
+                {
+                    uint32_t ay[3][4], bx[2][3][4];
+#pragma unroll
+                    for (int np = 0; np < 2; ++np)
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) ldsm4(bx[np][t], x_n + t * (C * C * 2) + np * 16 * C * 2);
+                    split_a<3>(y[0], y[1], ay);
+                    prod<3, 3, 2>(r, ay, bx);
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) ldsm4(bx[0][t], (x_n ^ 32) + t * (C * C * 2) + 16 * C * 2);
+                    split_a<3>(y[2], y[3], ay);
+                    prod2<3, 3>(r[2], r[3], ay, bx[0]);
+                }
+                if (MODE == STORE) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int tok = t_first + c * C + 8 * n + 2 * (lane & 3);
+                        float* to = a.errors + (static_cast<long long>(bh) * a.T + tok) * a.dv + col0 + 16 * grp + (lane >> 2);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (tok + (j & 1) < t_end) to[(j & 1) * a.dv + 8 * (j >> 1)] = r[n][j];
+                    }
+                }
+                // U^T for the outputs, and U^T e^(c_C - c) for the state
+                const float all = G->all;
+#pragma unroll
+                for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[n][j] *= all;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint32_t au[3][4], bt[DK / 16][KT][4];
+#pragma unroll
+                    for (int np = 0; np < DK / 16; ++np)
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+#pragma unroll
+                    for (int n = 2 * kk; n < 2 * kk + 2; ++n) {
+                        const float2 be = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? be.y : be.x;
+                    }
+                    if (MODE == OUT) {
+                        uint32_t ao[OT][4];
+                        split_a<OT>(r[2 * kk], r[2 * kk + 1], ao);
+#pragma unroll
+                        for (int t = 0; t < OT; ++t)
+                            reinterpret_cast<uint4*>(uf - lane * 2)[(kk * OT + t) * 32 + lane] = make_uint4(ao[t][0], ao[t][1], ao[t][2], ao[t][3]);
+                    }
+#pragma unroll
+                    for (int n = 2 * kk; n < 2 * kk + 2; ++n) {
+                        const float2 f = *reinterpret_cast<const float2*>(&G->left[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? f.y : f.x;
+                    }
+                    split_a<3>(r[2 * kk], r[2 * kk + 1], au);
+                    prod<3, KT, DK / 16>(S, au, bt);
+                }
+            } else {
             // this part's share of S0^T K^T, all tokens
             float y[4][4] = {};
 #pragma unroll
@@ -297,6 +394,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_walk(const WalkArgs 
                             ldsm4t(bt[kk][np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
                 }
                 prod<3, KT, DH / 16>(S, au, bt[kk]);
+            }
             }
             if (++stage == F::NS) stage = 0;
             if (++ostage == F::NO) ostage = 0;
