@@ -86,23 +86,27 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
 
 // Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
 // as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
-// takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step), the
-// fold (0.4 a segment) and the second walk.  Taken when a tenth is gained.
+// takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step, two
+// blocks an SM), the fold (0.4 a segment at d = 64, by d squared) and the second walk.  Taken when a
+// tenth is gained.  Forward at bf16, without and with the segments that it takes: 1x4x16384x64 578 and
+// 135 us (10 segments), 1x8x4096x64 154 and 74, 2x16x4096x64 168 and 159; 4x16x4096x64 fills the
+// machine: 188 without, 254 with three.
 Segments segments(const Problem& p) {
     constexpr int SMS = 148;
     const long long BH = static_cast<long long>(p.B) * p.H;
     const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16, fit = p.bf16 ? (p.d <= 64 ? 2 : 1) : (p.d == 32 ? 2 : 1);
-    const auto waves = [&](long long blocks) {
+    const auto waves = [&](long long blocks, int fit) {
         const long long rest = blocks % (SMS * fit);
         return (fit == 2 ? 1.25 : 1.0) * static_cast<double>(blocks / (SMS * fit)) + (rest == 0 ? 0.0 : rest <= SMS ? 1.0 : 1.25);
     };
+    const double fold_step = 0.4 * (p.d / 64.0) * (p.d / 64.0) + 0.1;
     int best = 1;
-    double cost = 0.9 * waves(BH * p.dv / CS) * NC;
+    double cost = 0.9 * waves(BH * p.dv / CS, fit) * NC;
     for (int n = 2; n <= 64 && n <= NC / 4; ++n) {
         const int chunks = (NC + n - 1) / n;
         if ((NC + chunks - 1) / chunks != n) continue;
-        const double c = 0.85 * chunks * waves(BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS) + 0.4 * n + 8 +
-                         chunks * waves(BH * n * p.dv / CS);
+        const long long summaries = BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS;
+        const double c = 0.85 * chunks * waves(summaries, 2) + fold_step * n + 8 + chunks * waves(BH * n * p.dv / CS, fit);
         if (c < cost) cost = c, best = n;
     }
     Segments g{best, (NC + best - 1) / best, 0, 0};

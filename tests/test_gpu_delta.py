@@ -142,9 +142,9 @@ def test_long_few_heads(dtype):
 @pytest.mark.parametrize("d,dv", [(32, 64), (64, 64), (128, 32), (128, 128)])
 def test_segments_of_a_padded_batch(dtype, d, dv):
     """Few heads and many tokens: the sequence is walked in segments, some of them behind an end."""
-    lens = torch.tensor([1000, 330, 0], dtype=torch.int32)
-    x = leaves(dtype, 3, 1, 1, 1000, d, dv, seed=14, state=True, slow=4.0)
-    assert hla.delta._library().hla_delta_kernel_launches(1 if dtype == "bf16" else 0, 3, 1, 1, 1000, d, dv) == 4
+    lens = torch.tensor([2000, 630, 0], dtype=torch.int32)
+    x = leaves(dtype, 3, 1, 1, 2000, d, dv, seed=14, state=True, slow=4.0)
+    assert hla.delta._library().hla_delta_kernel_launches(1 if dtype == "bf16" else 0, 3, 1, 1, 2000, d, dv) == 4
     want, last = od.forward(*x[:5], 0.2, x[5], lens)
     for b, n in enumerate(lens.tolist()):
         for t in x[:5]:

@@ -135,9 +135,9 @@ def test_long_and_many(dtype):
 @pytest.mark.parametrize("d,dv", [(32, 64), (64, 64), (128, 128)])
 def test_segments_of_a_padded_batch(dtype, d, dv):
     """Few heads and many tokens: both walks go in segments, some of them behind an end."""
-    lens = torch.tensor([1000, 330, 0], dtype=torch.int32)
-    x, dout, dstate = inputs(dtype, 3, 1, 1, 1000, d, dv, seed=15, slow=4.0)
-    assert hla.delta._library().hla_delta_backward_kernel_launches(1 if dtype == "bf16" else 0, 3, 1, 1, 1000, d, dv) == 8
+    lens = torch.tensor([2000, 630, 0], dtype=torch.int32)
+    x, dout, dstate = inputs(dtype, 3, 1, 1, 2000, d, dv, seed=15, slow=4.0)
+    assert hla.delta._library().hla_delta_backward_kernel_launches(1 if dtype == "bf16" else 0, 3, 1, 1, 2000, d, dv) == 8
     for b, n in enumerate(lens.tolist()):
         for t in (*x[:5], dout):
             t[b, :, n:] = 0.0
