@@ -898,7 +898,7 @@ Space space(const Problem& p) {
 template <typename F>
 cudaError_t start(const ReverseArgs& a, int blocks, cudaStream_t st) {
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
-    const cudaError_t e = cudaFuncSetAttribute(k_delta_reverse<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    const cudaError_t e = allow_smem<k_delta_reverse<F>>(F::bytes);
     if (e != cudaSuccess) return e;
     k_delta_reverse<F><<<blocks, F::WARPS * 32, F::bytes, st>>>(a);
     return cudaGetLastError();
@@ -936,11 +936,10 @@ cudaError_t block_grads(const Problem& p, const Gradients& gr, char* ws, const S
                       reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.R),
                       reinterpret_cast<float*>(ws + s.H), p.lengths, shared ? ws + s.dq : gr.dq, shared ? ws + s.dk : gr.dk,
                       gr.dv, gr.dg, gr.dbeta, p.B, p.Hk, p.H, p.T, blocks, p.bthd ? 1 : 0, p.scale};
-    void (*kernel)(const BlockArgs) = k_delta_block_grads<F, false>;
-    if (shared) kernel = k_delta_block_grads<F, true>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    const cudaError_t e = shared ? allow_smem<k_delta_block_grads<F, true>>(F::bytes) : allow_smem<k_delta_block_grads<F, false>>(F::bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<p.B * p.H * blocks, F::NT, F::bytes, st>>>(a);
+    if (shared) k_delta_block_grads<F, true><<<p.B * p.H * blocks, F::NT, F::bytes, st>>>(a);
+    else k_delta_block_grads<F, false><<<p.B * p.H * blocks, F::NT, F::bytes, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
 template <int DK, bool REV>
 cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
     constexpr int bytes = ((DK * (DK + 1) + 3) / 4 * 4 + DK * 16) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(k_delta_fold<DK, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem<k_delta_fold<DK, REV>>(bytes);
     if (e != cudaSuccess) return e;
     k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 16), DK * 4, bytes, st>>>(a);
     return cudaGetLastError();

@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 
 template <typename F>
 cudaError_t start(const WalkArgs& a, int blocks, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(k_delta_walk<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes);
+    cudaError_t e = allow_smem<k_delta_walk<F>>(F::bytes);
     if (e != cudaSuccess) return e;
     k_delta_walk<F><<<blocks, F::WARPS * 32, F::bytes, st>>>(a);
     return cudaGetLastError();

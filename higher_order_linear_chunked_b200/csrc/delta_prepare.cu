@@ -99,7 +99,7 @@ cudaError_t launch(const Problem& p, uint8_t* records, cudaStream_t st) {
     static_assert(F::bytes * F::WARPS <= 227 * 1024, "shared memory of a block");
     const int chunks = (p.T + C - 1) / C;
     const PrepArgs a{p.q, p.k, p.g, p.beta, p.lengths, records, p.B, p.Hk, p.H, p.T, chunks, p.bthd ? 1 : 0, p.scale};
-    cudaError_t e = cudaFuncSetAttribute(k_delta_prepare<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::bytes * F::WARPS);
+    cudaError_t e = allow_smem<k_delta_prepare<F>>(F::bytes * F::WARPS);
     if (e != cudaSuccess) return e;
     const long long n = static_cast<long long>(p.B) * p.H * chunks;
     k_delta_prepare<F><<<static_cast<unsigned>((n + F::WARPS - 1) / F::WARPS), F::WARPS * 32, F::bytes * F::WARPS, st>>>(a);

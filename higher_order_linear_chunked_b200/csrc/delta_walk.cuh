@@ -5,8 +5,24 @@
 #pragma once
 #include "delta_mma.cuh"
 
+#include <atomic>
+
 namespace hla {
 namespace delta {
+
+// Dynamic shared memory of a kernel, asked for once a device (the attribute stays with the device).
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 constexpr int kMS = 36;                      // floats of a row of the transposed system
 

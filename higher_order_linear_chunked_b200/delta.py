@@ -61,7 +61,8 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # both None in a torch without CUDA
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 class _On:
@@ -81,7 +82,7 @@ class _On:
                     t.record_stream(self.given)
 
     def call(self, fn, what, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if _current_device() == self.device.index:
             rc = fn(*args)
         else:
             with torch.cuda.device(self.device):
@@ -129,10 +130,11 @@ def _leaves(q, k, v, g, beta, layout, step=False):
         lead = (B, T, H)
     else:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+    on = q.get_device()
     if not (k.shape == q.shape and v.shape == (*lead, dv) and g.shape == lead and beta.shape == lead and
             k.dtype is dt and v.dtype is dt and g.dtype is torch.float32 and beta.dtype is torch.float32 and
-            k.device == dev and v.device == dev and g.device == dev and beta.device == dev and q.is_contiguous() and
-            k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
+            k.get_device() == on and v.get_device() == on and g.get_device() == on and beta.get_device() == on and
+            q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
         _expect("q", q, tuple(q.shape), dt, dev)
         _expect("k", k, tuple(q.shape), dt, dev)
         _expect("v", v, (*lead, dv), dt, dev)
