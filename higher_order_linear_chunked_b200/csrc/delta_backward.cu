@@ -42,8 +42,9 @@ struct Rev {
     static constexpr int DK = DK_, CS = 16 * NG_;
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;
-    static constexpr int AHEAD = BF ? 3 : 1, NS = AHEAD + 1, NLD = BF ? 2 : 4;
-    static constexpr int NH = DK_ == 128 ? 4 : 2, W_STATE = NH * NG_, WARPS = W_STATE + NLD;
+    static constexpr int AHEAD = BF ? 2 : 1, NS = AHEAD + 1, NLD = BF ? 2 : 4;
+    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2),   // as in the forward walk
+                          W_STATE = NH * NG_, WARPS = W_STATE + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2, OTILE = KT * C * CS * 2, PB = 3 * C * C * 2;
     // a stage
     static constexpr int k = 0, q = k + KTILE, x = q + KTILE, p = x + kXBytes, dO = p + PB, gates = dO + OTILE;
@@ -52,13 +53,14 @@ struct Rev {
     static constexpr int YB = 2 * 3 * 512;
     static constexpr int yf = ex + W_STATE * 2048;      // dU as an A operand
     static constexpr int wf = yf + NG_ * YB;            // scale e^c dO as an A operand
-    static constexpr int bytes = wf + NG_ * YB;
+    static constexpr int bytes = NH > 1 ? wf + NG_ * YB : ex;
+    static constexpr int BLOCKS = bytes <= 113 * 1024 ? 2 : 1;   // of an SM
 };
 
 template <typename F>
-__global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const ReverseArgs a) {
+__global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(const ReverseArgs a) {
     using E = typename F::Elem;
-    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / NH, CS = F::CS, KT = F::KT;
+    constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / (NH == 1 ? 2 : NH), CS = F::CS, KT = F::KT;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,6 +112,113 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
 #pragma unroll
                     for (int j = 0; j < 4; ++j) to[static_cast<long long>(8 * n + (j & 1)) * a.dv + 8 * (j >> 1)] = S[n][j];
             }
+            if constexpr (NH == 1) {
+                // one warp has the whole key axis: everything stays in its registers
+                float y[4][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    uint32_t bk[2][KT][4], as[3][4];
+#pragma unroll
+                    for (int np = 0; np < 2; ++np)
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            ldsm4(bk[np][t], ((k_n + so) ^ (ks << 5)) + t * (C * DK * 2) + np * 16 * DK * 2);
+                    split_a<3>(S[2 * ks], S[2 * ks + 1], as);
+                    prod<3, KT, 2>(y, as, bk);
+                }
+                // dU^T = dO^T P + (dS^T K^T) e^(c_C - c); P[i][j] is zero for j > i
+                uint32_t ao[2][KT][4];
+                float z[4][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+                        ldsm4t(ao[kk][t], sb + F::dO + so + t * (C * CS * 2) +
+                                              piece<CS * 2>(16 * kk + (lane >> 4) * 8 + (lane & 7), 2 * grp + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int np = 0; np <= kk; ++np) {
+                        uint32_t bp[3][4];
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            ldsm4t(bp[t], at_rows_first<C * 2>(sb + F::p + so + t * (C * C * 2), 16 * kk, 2 * np, lane));
+                        prod2<KT, 3>(z[2 * np], z[2 * np + 1], ao[kk], bp);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 f = *reinterpret_cast<const float2*>(&G->left[8 * n + 2 * (lane & 3)]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[n][j] = fmaf((j & 1) ? f.y : f.x, y[n][j], z[n][j]);
+                }
+                const float all = G->all;
+#pragma unroll
+                for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[n][j] *= all;
+                // H^T = dU^T X'; X'[j][i] is zero for j < i
+                float r[4][4] = {};
+#pragma unroll
+                for (int kk = 1; kk >= 0; --kk) {
+                    uint32_t ay[3][4];
+                    split_a<3>(z[2 * kk], z[2 * kk + 1], ay);
+#pragma unroll
+                    for (int np = 0; np <= kk; ++np) {
+                        uint32_t bx[3][4];
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            ldsm4t(bx[t], at_rows_first<C * 2>(sb + F::x + so + t * (C * C * 2), 16 * kk, 2 * np, lane));
+                        prod2<3, 3>(r[2 * np], r[2 * np + 1], ay, bx);
+                    }
+                }
+                if (!F::SUMMARY) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int tok = c * C + 8 * n + 2 * (lane & 3);
+                        float* to = a.H + (static_cast<long long>(bh) * a.T + tok) * a.dv + own_col;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (tok + (j & 1) < T) to[(j & 1) * a.dv + 8 * (j >> 1)] = r[n][j];
+                    }
+                }
+                // dS0^T: scale (e^c Q)^T dO and -(e^c K)^T Z, transposed
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint32_t au[3][4], bt[DK / 16][KT][4];
+                    float w[2][4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = *reinterpret_cast<const float2*>(&G->since[16 * kk + 8 * e + 2 * (lane & 3)]);
+                        const float2 be = *reinterpret_cast<const float2*>(&G->beta[16 * kk + 8 * e + 2 * (lane & 3)]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {     // registers 2 e + h: columns + 8 h of tile e
+                            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                            for (int t = KT - 1; t >= 0; --t) {
+                                x0 += __uint_as_float(ao[kk][t][2 * e + h] << 16);
+                                x1 += __uint_as_float(ao[kk][t][2 * e + h] & 0xffff0000u);
+                            }
+                            w[e][2 * h] = a.scale * f.x * x0;
+                            w[e][2 * h + 1] = a.scale * f.y * x1;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[2 * kk + e][j] *= (j & 1) ? -f.y * be.y : -f.x * be.x;
+                    }
+#pragma unroll
+                    for (int np = 0; np < DK / 16; ++np)
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            ldsm4t(bt[np][t], ((q_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                    split_a<3>(w[0], w[1], au);
+                    prod<3, KT, DK / 16>(S, au, bt);
+#pragma unroll
+                    for (int np = 0; np < DK / 16; ++np)
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+                            ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                    split_a<3>(r[2 * kk], r[2 * kk + 1], au);
+                    prod<3, KT, DK / 16>(S, au, bt);
+                }
+            } else {
             // this part's share of dS^T K^T, all tokens
             float y[4][4] = {};
 #pragma unroll
@@ -281,6 +390,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, 1) k_delta_reverse(const Revers
                     for (int t = 0; t < KT; ++t)
                         ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
                 prod<3, KT, DH / 16>(S, au, bt);
+            }
             }
             if (++stage == F::NS) stage = 0;
             step_end();
@@ -507,6 +617,7 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
                                            float f, int lane, int warp, int gt = 0, float* rows = nullptr, float* cols = nullptr) {
     constexpr int DK = F::DK, DV = F::DV, KT = F::KT;
     const int r0 = warp * 16;
+    const float2 own[2] = {sum[r0 + (lane >> 2)], sum[r0 + 8 + (lane >> 2)]};
 #pragma unroll 1
     for (int jb = ROWS ? 0 : warp; jb <= (ROWS ? warp : F::WARPS - 1); ++jb) {
         float w[2][4] = {};
@@ -519,15 +630,20 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
             for (int t = 0; t < YT; ++t) ldsm4(y[t], at_pieces_first<DV * 2>(sb + yt + t * F::OTERM, 16 * jb, 2 * ks, lane));
             prod2<AT, YT>(w[0], w[1], x, y);
         }
+        const bool diagonal = jb == warp;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n) {
+            const float4 his = *reinterpret_cast<const float4*>(&sum[16 * jb + 8 * n + 2 * (lane & 3)]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int mine = r0 + (lane >> 2) + 8 * (j >> 1), other = 16 * jb + 8 * n + 2 * (lane & 3) + (j & 1);
-                const int i = ROWS ? mine : other, k = ROWS ? other : mine;
-                const float2 x = sum[i], y = sum[k];
-                w[n][j] = (STRICT ? k < i : k <= i) ? f * w[n][j] * ex2((x.x - y.x) + (x.y - y.y)) : 0.f;
+                const float2 other = (j & 1) ? make_float2(his.z, his.w) : make_float2(his.x, his.y);
+                const float gap = (own[j >> 1].x - other.x) + (own[j >> 1].y - other.y);
+                w[n][j] *= f * ex2(ROWS ? gap : -gap);
+                // this lane's row and column within the block: off the diagonal block all count
+                const int lead = (lane >> 2) + 8 * (j >> 1) - (8 * n + 2 * (lane & 3) + (j & 1));
+                if (diagonal && !(ROWS ? (STRICT ? lead > 0 : lead >= 0) : (STRICT ? lead < 0 : lead <= 0))) w[n][j] = 0.f;
             }
+        }
         if constexpr (ROWS) {
             float g[2][4] = {};
 #pragma unroll 2
