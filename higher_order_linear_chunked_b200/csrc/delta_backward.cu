@@ -42,9 +42,11 @@ struct Rev {
     static constexpr int DK = DK_, CS = 16 * NG_;
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;
-    static constexpr int AHEAD = BF ? 2 : 1, NS = AHEAD + 1, NLD = BF ? 2 : 4;
-    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2),   // as in the forward walk
-                          W_STATE = NH * NG_, WARPS = W_STATE + NLD;
+    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2);   // as in the forward walk
+    // with one state warp a group, another one takes the outputs' share of dS, a chunk ahead of it
+    static constexpr int W_SIDE = NH == 1 ? NG_ : 0;
+    static constexpr int AHEAD = (BF ? 2 : 1) + (W_SIDE ? 1 : 0), NS = AHEAD + 1, NLD = BF ? 2 : 4;
+    static constexpr int W_STATE = NH * NG_, WARPS = W_STATE + W_SIDE + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2, OTILE = KT * C * CS * 2, PB = 3 * C * C * 2;
     // a stage
     static constexpr int k = 0, q = k + KTILE, x = q + KTILE, p = x + kXBytes, dO = p + PB, gates = dO + OTILE;
@@ -53,7 +55,9 @@ struct Rev {
     static constexpr int YB = 2 * 3 * 512;
     static constexpr int yf = ex + W_STATE * 2048;      // dU as an A operand
     static constexpr int wf = yf + NG_ * YB;            // scale e^c dO as an A operand
-    static constexpr int bytes = NH > 1 ? wf + NG_ * YB : ex;
+    static constexpr int side = ex;                     // or the outputs' share of two chunks
+    static constexpr int SIDE = NG_ * (DK_ / 8) * 512;
+    static constexpr int bytes = NH > 1 ? wf + NG_ * YB : side + 2 * SIDE;
     static constexpr int BLOCKS = bytes <= 113 * 1024 ? 2 : 1;   // of an SM
 };
 
@@ -74,12 +78,12 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
     const int chunks = max(0, c_end - c_first);
     const int blocks = (all_chunks + a.block_chunks - 1) / a.block_chunks;
     const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.Hv);
-    constexpr int w_load = F::W_STATE;
+    constexpr int w_side = F::W_STATE, w_load = w_side + F::W_SIDE;
     const int grp = warp / NH, part = warp % NH;
 
     float S[DH / 8][4];                                 // dS^T, as the forward walk holds S^T
     const int own_col = col0 + 16 * grp + (lane >> 2), own_key = part * DH + 2 * (lane & 3);
-    if (warp < w_load) {
+    if (warp < w_side) {
         const float* from = nullptr;
         if (a.behind && !F::SUMMARY) from = a.behind + (static_cast<long long>(bh) * a.segments + seg) * DK * a.dv;
         if (a.behind && F::SUMMARY && seg == a.segments - 1) from = a.behind + static_cast<long long>(bh) * DK * a.dv;
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
     }
     constexpr int ALL = F::WARPS * 32;
     const auto step_end = [] { ptx::named_sync(15, ALL); };
-    if (chunks > 0 && warp < w_load) {
+    if (chunks > 0 && warp < w_side) {
         const uint32_t k_n = at_pieces_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
         const uint32_t k_t = at_rows_first<DK * 2>(sb + F::k, 0, part * (DH / 8), lane);
         const uint32_t q_t = at_rows_first<DK * 2>(sb + F::q, 0, part * (DH / 8), lane);
@@ -180,41 +184,30 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
                             if (tok + (j & 1) < T) to[(j & 1) * a.dv + 8 * (j >> 1)] = r[n][j];
                     }
                 }
-                // dS0^T: scale (e^c Q)^T dO and -(e^c K)^T Z, transposed
+                // dS0^T: the outputs' share from the side warp, and -(e^c K)^T Z, transposed
+                {
+                    const float4* sd = reinterpret_cast<const float4*>(sm + F::side + (c & 1) * F::SIDE) + grp * (DK / 8) * 32 + lane;
+#pragma unroll
+                    for (int n = 0; n < DK / 8; ++n) {
+                        const float4 x = sd[n * 32];
+                        S[n][0] += x.x; S[n][1] += x.y; S[n][2] += x.z; S[n][3] += x.w;
+                    }
+                }
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     uint32_t au[3][4], bt[DK / 16][KT][4];
-                    float w[2][4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 f = *reinterpret_cast<const float2*>(&G->since[16 * kk + 8 * e + 2 * (lane & 3)]);
-                        const float2 be = *reinterpret_cast<const float2*>(&G->beta[16 * kk + 8 * e + 2 * (lane & 3)]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {     // registers 2 e + h: columns + 8 h of tile e
-                            float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-                            for (int t = KT - 1; t >= 0; --t) {
-                                x0 += __uint_as_float(ao[kk][t][2 * e + h] << 16);
-                                x1 += __uint_as_float(ao[kk][t][2 * e + h] & 0xffff0000u);
-                            }
-                            w[e][2 * h] = a.scale * f.x * x0;
-                            w[e][2 * h + 1] = a.scale * f.y * x1;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) r[2 * kk + e][j] *= (j & 1) ? -f.y * be.y : -f.x * be.x;
-                    }
-#pragma unroll
-                    for (int np = 0; np < DK / 16; ++np)
-#pragma unroll
-                        for (int t = 0; t < KT; ++t)
-                            ldsm4t(bt[np][t], ((q_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
-                    split_a<3>(w[0], w[1], au);
-                    prod<3, KT, DK / 16>(S, au, bt);
 #pragma unroll
                     for (int np = 0; np < DK / 16; ++np)
 #pragma unroll
                         for (int t = 0; t < KT; ++t)
                             ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = *reinterpret_cast<const float2*>(&G->since[16 * kk + 8 * e + 2 * (lane & 3)]);
+                        const float2 be = *reinterpret_cast<const float2*>(&G->beta[16 * kk + 8 * e + 2 * (lane & 3)]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[2 * kk + e][j] *= (j & 1) ? -f.y * be.y : -f.x * be.x;
+                    }
                     split_a<3>(r[2 * kk], r[2 * kk + 1], au);
                     prod<3, KT, DK / 16>(S, au, bt);
                 }
@@ -395,6 +388,54 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
             if (++stage == F::NS) stage = 0;
             step_end();
         }
+    } else if (chunks > 0 && warp < w_load) {
+        // scale (e^c Q)^T dO, transposed: what the outputs of a chunk add to dS, a step before the state
+        const int g = warp - w_side;
+        const uint32_t q_t = at_rows_first<DK * 2>(sb + F::q, 0, 0, lane);
+        int stage = 0;
+        for (int s = -F::AHEAD; s < -1; ++s) step_end();
+        for (int c = c_end - 1; c >= c_first; --c) {
+            const uint32_t so = stage * F::STAGE;
+            const Gates* G = reinterpret_cast<const Gates*>(sm + stage * F::STAGE + F::gates);
+            float W[DK / 8][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t ao[KT][4], au[3][4], bt[DK / 16][KT][4];
+                float w[2][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+                    ldsm4t(ao[t], sb + F::dO + so + t * (C * CS * 2) +
+                                      piece<CS * 2>(16 * kk + (lane >> 4) * 8 + (lane & 7), 2 * g + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int np = 0; np < DK / 16; ++np)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+                        ldsm4t(bt[np][t], ((q_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 f = *reinterpret_cast<const float2*>(&G->since[16 * kk + 8 * e + 2 * (lane & 3)]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {     // registers 2 e + h: columns + 8 h of tile e
+                        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                        for (int t = KT - 1; t >= 0; --t) {
+                            x0 += __uint_as_float(ao[t][2 * e + h] << 16);
+                            x1 += __uint_as_float(ao[t][2 * e + h] & 0xffff0000u);
+                        }
+                        w[e][2 * h] = a.scale * f.x * x0;
+                        w[e][2 * h + 1] = a.scale * f.y * x1;
+                    }
+                }
+                split_a<3>(w[0], w[1], au);
+                prod<3, KT, DK / 16>(W, au, bt);
+            }
+            float4* sd = reinterpret_cast<float4*>(sm + F::side + (c & 1) * F::SIDE) + g * (DK / 8) * 32 + lane;
+#pragma unroll
+            for (int n = 0; n < DK / 8; ++n) sd[n * 32] = make_float4(W[n][0], W[n][1], W[n][2], W[n][3]);
+            if (++stage == F::NS) stage = 0;
+            step_end();
+        }
+        step_end();
     } else if (chunks > 0) {
         const int lt = (warp - w_load) * 32 + lane;
         constexpr int LT = F::NLD * 32, REC = record_bytes(2, 3);
@@ -418,13 +459,13 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
                 if (++stage == F::NS) stage = 0;
             }
             cp_commit();
-            cp_wait<F::AHEAD - 1>();
+            cp_wait<F::AHEAD - 1 - (F::W_SIDE ? 1 : 0)>();
             step_end();
         }
     }
     float* const to = F::SUMMARY ? a.back + (static_cast<long long>(bh) * a.segments + seg) * DK * a.dv
                                  : (a.dstate_in && seg == 0 ? a.dstate_in + static_cast<long long>(bh) * DK * a.dv : nullptr);
-    if (warp < w_load && to) {
+    if (warp < w_side && to) {
 #pragma unroll
         for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
