@@ -661,7 +661,7 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
     const float2 own[2] = {sum[r0 + (lane >> 2)], sum[r0 + 8 + (lane >> 2)]};
 #pragma unroll 1
     for (int jb = ROWS ? 0 : warp; jb <= (ROWS ? warp : F::WARPS - 1); ++jb) {
-        float w[2][4] = {};
+        float w[2][4] = {}, low[2][4] = {};
 #pragma unroll 2
         for (int ks = 0; ks < DV / 16; ++ks) {
             uint32_t x[AT][4], y[YT][4];
@@ -669,8 +669,10 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
             for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, 2 * ks, lane));
 #pragma unroll
             for (int t = 0; t < YT; ++t) ldsm4(y[t], at_pieces_first<DV * 2>(sb + yt + t * F::OTERM, 16 * jb, 2 * ks, lane));
-            prod2<AT, YT>(w[0], w[1], x, y);
+            prod2<AT, YT>(w[0], w[1], low[0], low[1], x, y);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[0][j] += low[0][j], w[1][j] += low[1][j];
         const bool diagonal = jb == warp;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -686,7 +688,7 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
             }
         }
         if constexpr (ROWS) {
-            float g[2][4] = {};
+            float g[2][4] = {}, glow[2][4] = {};
 #pragma unroll 2
             for (int ks = 0; ks < DK / 16; ++ks) {
                 uint32_t x[KT][4], y[KT][4];
@@ -694,7 +696,12 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
                 for (int t = 0; t < KT; ++t) ldsm4(x[t], at_rows_first<DK * 2>(sb + gt + t * F::KTERM, r0, 2 * ks, lane));
 #pragma unroll
                 for (int t = 0; t < KT; ++t) ldsm4(y[t], at_pieces_first<DK * 2>(sb + bt + t * F::KTERM, 16 * jb, 2 * ks, lane));
-                prod2<KT, KT>(g[0], g[1], x, y);
+                if constexpr (KT == 1) prod2<KT, KT>(g[0], g[1], x, y);
+                else prod2<KT, KT>(g[0], g[1], glow[0], glow[1], x, y);
+            }
+            if constexpr (KT > 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[0][j] += glow[0][j], g[1][j] += glow[1][j];
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {

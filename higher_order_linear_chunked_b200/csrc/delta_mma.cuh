@@ -74,6 +74,26 @@ __device__ __forceinline__ void prod2(float (&c0)[4], float (&c1)[4], const uint
         }
 }
 
+// The same with the leading products and the small ones summed apart (add the two at the end): a long
+// axis then cuts at the large sum's last bit once a step, not once a product.
+template <int AT, int BT>
+__device__ __forceinline__ void prod2(float (&h0)[4], float (&h1)[4], float (&l0)[4], float (&l1)[4],
+                                      const uint32_t (&a)[AT][4], const uint32_t (&b)[BT][4]) {
+    constexpr int M = AT > BT ? AT : BT;
+#pragma unroll
+    for (int d = M - 1; d > 0; --d)
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            const int j = d - i;
+            if (j >= 0 && j < BT) {
+                mma16816(l0, a[i], b[j][0], b[j][1]);
+                mma16816(l1, a[i], b[j][2], b[j][3]);
+            }
+        }
+    mma16816(h0, a[0], b[0][0], b[0][1]);
+    mma16816(h1, a[0], b[0][2], b[0][3]);
+}
+
 // The bf16 terms of a pair, packed (x0 in the low half).
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&t)[N]) {

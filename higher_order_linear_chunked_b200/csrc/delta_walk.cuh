@@ -175,7 +175,7 @@ template <int DK, int KT, int PT>
 __device__ __forceinline__ void products(bool keys, bool rowbeta, uint32_t kt, uint32_t at, const float2* sum, const float* beta,
                                          float* mt, uint8_t* pt, float scale, int p, int lane) {
     constexpr int RB = DK * 2, TERM = C * DK * 2;
-    float acc[4][4] = {};
+    float acc[4][4] = {}, low[4][4] = {};
 #pragma unroll(DK > 32 ? 2 : 1)
     for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t a[KT][4];
@@ -187,8 +187,15 @@ __device__ __forceinline__ void products(bool keys, bool rowbeta, uint32_t kt, u
             uint32_t b[KT][4];
 #pragma unroll
             for (int t = 0; t < KT; ++t) ldsm4(b[t], at_pieces_first<RB>(kt + t * TERM, 16 * np, 2 * ks, lane));
-            prod2<KT, KT>(acc[2 * np], acc[2 * np + 1], a, b);
+            if constexpr (KT == 1) prod2<KT, KT>(acc[2 * np], acc[2 * np + 1], a, b);
+            else prod2<KT, KT>(acc[2 * np], acc[2 * np + 1], low[2 * np], low[2 * np + 1], a, b);
         }
+    }
+    if constexpr (KT > 1) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[n][j] += low[n][j];
     }
     float2 ci[2];
     float fi[2];
