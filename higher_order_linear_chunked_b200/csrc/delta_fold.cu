@@ -11,16 +11,17 @@ struct FoldArgs {
     int dv, count;
 };
 
-// S <- A S + B from segment to segment (REV: S <- A^T S + G, from the last to the first), 16 columns of
-// one head a block; a thread has four columns of one row, the next segment's A is on its way meanwhile.
-// fp32 on the CUDA cores: a segment costs 2 d d 16 flops a block, a small part of a walk over it.
+// S <- A S + B from segment to segment (REV: S <- A^T S + G, from the last to the first), 8 columns of
+// one head a block; a thread has four columns of one row.  A segment's A and B are on their way while
+// the one before is worked on: what is left of a segment is 2 d d 8 flops a block on the CUDA cores (fp32)
+// and two barriers, about 0.4 us at d = 64.
 template <int DK, bool REV>
-__global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
-    constexpr int NT = DK * 4, LD = DK + 1, U = DK * DK / 4 / NT;      // float4 of A a thread
+__global__ void __launch_bounds__(DK * 2) k_delta_fold(const FoldArgs a) {
+    constexpr int NT = DK * 2, LD = DK + 1, U = DK * DK / 4 / NT;      // float4 of A a thread
     extern __shared__ __align__(16) float sm[];
     float* As = sm;                                                    // [k][row]
-    float4* Ss = reinterpret_cast<float4*>(sm + (DK * LD + 3) / 4 * 4);   // [k][4 x 4 columns]
-    const int slices = a.dv / 16, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * 16;
+    float4* Ss = reinterpret_cast<float4*>(sm + (DK * LD + 3) / 4 * 4);   // [k][2 x 4 columns]
+    const int slices = a.dv / 8, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * 8;
     const int tid = threadIdx.x, r = tid % DK, cg = tid / DK, width = a.dv + DK;
     const int N = a.count;
     const auto A = [&](int s) { return a.sums + (static_cast<long long>(bh) * (N - 1) + s) * DK * width + a.dv; };
@@ -32,12 +33,8 @@ __global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
         store4(a.out + ((static_cast<long long>(bh) * N + s) * DK + r) * a.dv + col0 + 4 * cg, x);
     };
     const int step = REV ? -1 : 1, s0 = REV ? N - 1 : 0, last = REV ? 0 : N - 1;
-    float cur[4] = {};
-    if (a.first) load4(a.first + (static_cast<long long>(bh) * DK + r) * a.dv + col0 + 4 * cg, cur);
-    put(s0, cur);
-    load4(add(s0), cur);
-    put(s0 + step, cur);
     float4 next[U];
+    float plus[4];
     const auto ask = [&](int s) {
         if (s == last) return;
 #pragma unroll
@@ -45,8 +42,14 @@ __global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
             const int i = tid + u * NT;
             next[u] = *reinterpret_cast<const float4*>(A(s) + (i / (DK / 4)) * width + (i % (DK / 4)) * 4);
         }
+        load4(add(s), plus);
     };
     ask(s0 + step);
+    float cur[4] = {};
+    if (a.first) load4(a.first + (static_cast<long long>(bh) * DK + r) * a.dv + col0 + 4 * cg, cur);
+    put(s0, cur);
+    load4(add(s0), cur);
+    put(s0 + step, cur);
     for (int s = s0 + step; s != last; s += step) {
         __syncthreads();
 #pragma unroll
@@ -56,29 +59,33 @@ __global__ void __launch_bounds__(DK * 4) k_delta_fold(const FoldArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) As[REV ? row * LD + c + j : (c + j) * LD + row] = x[j];
         }
-        Ss[r * 4 + cg] = make_float4(cur[0], cur[1], cur[2], cur[3]);
+        Ss[r * 2 + cg] = make_float4(cur[0], cur[1], cur[2], cur[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cur[j] = plus[j];
         __syncthreads();
         ask(s + step);
-        load4(add(s), cur);
+        float odd[4] = {};
 #pragma unroll 16
-        for (int k = 0; k < DK; ++k) {
-            const float x = As[k * LD + r];
-            const float4 y = Ss[k * 4 + cg];
-            cur[0] = fmaf(x, y.x, cur[0]);
-            cur[1] = fmaf(x, y.y, cur[1]);
-            cur[2] = fmaf(x, y.z, cur[2]);
-            cur[3] = fmaf(x, y.w, cur[3]);
+        for (int k = 0; k < DK; k += 2) {
+            const float x0 = As[k * LD + r], x1 = As[(k + 1) * LD + r];
+            const float4 y0 = Ss[k * 2 + cg], y1 = Ss[(k + 1) * 2 + cg];
+            cur[0] = fmaf(x0, y0.x, cur[0]); odd[0] = fmaf(x1, y1.x, odd[0]);
+            cur[1] = fmaf(x0, y0.y, cur[1]); odd[1] = fmaf(x1, y1.y, odd[1]);
+            cur[2] = fmaf(x0, y0.z, cur[2]); odd[2] = fmaf(x1, y1.z, odd[2]);
+            cur[3] = fmaf(x0, y0.w, cur[3]); odd[3] = fmaf(x1, y1.w, odd[3]);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cur[j] += odd[j];
         put(s + step, cur);
     }
 }
 
 template <int DK, bool REV>
 cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
-    constexpr int bytes = ((DK * (DK + 1) + 3) / 4 * 4 + DK * 16) * 4;
+    constexpr int bytes = ((DK * (DK + 1) + 3) / 4 * 4 + DK * 8) * 4;
     const cudaError_t e = allow_smem<k_delta_fold<DK, REV>>(bytes);
     if (e != cudaSuccess) return e;
-    k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 16), DK * 4, bytes, st>>>(a);
+    k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 8), DK * 2, bytes, st>>>(a);
     return cudaGetLastError();
 }
 
