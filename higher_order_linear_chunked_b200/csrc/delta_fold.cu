@@ -12,77 +12,90 @@ struct FoldArgs {
 };
 
 // S <- A S + B from segment to segment (REV: S <- A^T S + G, from the last to the first), 8 columns of
-// one head a block; a thread has four columns of one row.  A segment's A and B are on their way while
-// the one before is worked on: what is left of a segment is 2 d d 8 flops a block on the CUDA cores (fp32)
-// and two barriers, about 0.4 us at d = 64.
+// one head a block; a thread has four columns of one row.  A and B of the next two segments are on
+// their way into a ring of three; a segment then costs 2 d d 8 flops a block on the CUDA cores (fp32)
+// and one barrier: 0.8 us at d = 64, bound by the four warps' own latency (four lanes to a row, with
+// 16 warps, took 1.1: the barrier and the copies weigh more than the products).
+template <int DK>
+struct FoldSmem {
+    static constexpr int LD = DK + 4, A = DK * LD, STAGE = A + DK * 8, S = 3 * STAGE, floats = S + 2 * DK * 8;
+};
+
 template <int DK, bool REV>
 __global__ void __launch_bounds__(DK * 2) k_delta_fold(const FoldArgs a) {
-    constexpr int NT = DK * 2, LD = DK + 1, U = DK * DK / 4 / NT;      // float4 of A a thread
+    using M = FoldSmem<DK>;
+    constexpr int NT = DK * 2, LD = M::LD;
     extern __shared__ __align__(16) float sm[];
-    float* As = sm;                                                    // [k][row]
-    float4* Ss = reinterpret_cast<float4*>(sm + (DK * LD + 3) / 4 * 4);   // [k][2 x 4 columns]
+    const uint32_t sb = ptx::smem_u32(sm);
     const int slices = a.dv / 8, bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * 8;
     const int tid = threadIdx.x, r = tid % DK, cg = tid / DK, width = a.dv + DK;
-    const int N = a.count;
-    const auto A = [&](int s) { return a.sums + (static_cast<long long>(bh) * (N - 1) + s) * DK * width + a.dv; };
-    const auto add = [&](int s) {
-        return REV ? a.back + ((static_cast<long long>(bh) * N + s) * DK + r) * a.dv + col0 + 4 * cg
-                   : a.sums + ((static_cast<long long>(bh) * (N - 1) + s) * DK + r) * width + col0 + 4 * cg;
+    const int N = a.count, step = REV ? -1 : 1, s0 = REV ? N - 1 : 0, last = REV ? 0 : N - 1;
+    const auto added = [&](int s) {      // B or G of segment s, this block's columns
+        return REV ? a.back + (static_cast<long long>(bh) * N + s) * DK * a.dv + col0
+                   : a.sums + (static_cast<long long>(bh) * (N - 1) + s) * DK * width + col0;
     };
+    const int bstep = REV ? a.dv : width;
     const auto put = [&](int s, const float (&x)[4]) {
         store4(a.out + ((static_cast<long long>(bh) * N + s) * DK + r) * a.dv + col0 + 4 * cg, x);
     };
-    const int step = REV ? -1 : 1, s0 = REV ? N - 1 : 0, last = REV ? 0 : N - 1;
-    float4 next[U];
-    float plus[4];
-    const auto ask = [&](int s) {
-        if (s == last) return;
+    const auto ask = [&](int n) {        // the n-th segment of the fold into its stage
+        const int s = s0 + n * step;
+        if (n < N - 1) {
+            const uint32_t to = sb + (n % 3) * M::STAGE * 4;
+            const float* A = a.sums + (static_cast<long long>(bh) * (N - 1) + s) * DK * width + a.dv;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = tid + u * NT;
-            next[u] = *reinterpret_cast<const float4*>(A(s) + (i / (DK / 4)) * width + (i % (DK / 4)) * 4);
+            for (int i = tid; i < DK * DK / 4; i += NT)
+                cp_async16(to + ((i / (DK / 4)) * LD + (i % (DK / 4)) * 4) * 4, A + (i / (DK / 4)) * width + (i % (DK / 4)) * 4, true);
+            cp_async16(to + (M::A + r * 8 + 4 * cg) * 4, added(s) + r * bstep + 4 * cg, true);
         }
-        load4(add(s), plus);
+        cp_commit();
     };
-    ask(s0 + step);
+    ask(1);
+    ask(2);
     float cur[4] = {};
     if (a.first) load4(a.first + (static_cast<long long>(bh) * DK + r) * a.dv + col0 + 4 * cg, cur);
     put(s0, cur);
-    load4(add(s0), cur);
+    load4(added(s0) + r * bstep + 4 * cg, cur);
     put(s0 + step, cur);
-    for (int s = s0 + step; s != last; s += step) {
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = tid + u * NT, row = i / (DK / 4), c = (i % (DK / 4)) * 4;
-            const float x[4] = {next[u].x, next[u].y, next[u].z, next[u].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) As[REV ? row * LD + c + j : (c + j) * LD + row] = x[j];
-        }
+    for (int n = 1; s0 + n * step != last; ++n) {
+        float4* Ss = reinterpret_cast<float4*>(sm + M::S + (n & 1) * DK * 8);
+        const float* As = sm + (n % 3) * M::STAGE;
         Ss[r * 2 + cg] = make_float4(cur[0], cur[1], cur[2], cur[3]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cur[j] = plus[j];
+        cp_wait<1>();
         __syncthreads();
-        ask(s + step);
+        ask(n + 2);                      // its stage was last read before this barrier
+        load4(As + M::A + r * 8 + 4 * cg, cur);
         float odd[4] = {};
 #pragma unroll 16
-        for (int k = 0; k < DK; k += 2) {
-            const float x0 = As[k * LD + r], x1 = As[(k + 1) * LD + r];
-            const float4 y0 = Ss[k * 2 + cg], y1 = Ss[(k + 1) * 2 + cg];
-            cur[0] = fmaf(x0, y0.x, cur[0]); odd[0] = fmaf(x1, y1.x, odd[0]);
-            cur[1] = fmaf(x0, y0.y, cur[1]); odd[1] = fmaf(x1, y1.y, odd[1]);
-            cur[2] = fmaf(x0, y0.z, cur[2]); odd[2] = fmaf(x1, y1.z, odd[2]);
-            cur[3] = fmaf(x0, y0.w, cur[3]); odd[3] = fmaf(x1, y1.w, odd[3]);
+        for (int k = 0; k < DK; k += 4) {
+            float x[4];
+            if (REV) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = As[(k + j) * LD + r];
+            } else {
+                load4(As + r * LD + k, x);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 y = Ss[(k + j) * 2 + cg];
+                float (&to)[4] = (j & 1) ? odd : cur;
+                to[0] = fmaf(x[j], y.x, to[0]);
+                to[1] = fmaf(x[j], y.y, to[1]);
+                to[2] = fmaf(x[j], y.z, to[2]);
+                to[3] = fmaf(x[j], y.w, to[3]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) cur[j] += odd[j];
-        put(s + step, cur);
+        put(s0 + (n + 1) * step, cur);
     }
+    cp_wait<0>();
 }
 
 template <int DK, bool REV>
 cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
-    constexpr int bytes = ((DK * (DK + 1) + 3) / 4 * 4 + DK * 8) * 4;
+    constexpr int bytes = FoldSmem<DK>::floats * 4;
+    static_assert(bytes <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = allow_smem<k_delta_fold<DK, REV>>(bytes);
     if (e != cudaSuccess) return e;
     k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 8), DK * 2, bytes, st>>>(a);
@@ -94,10 +107,10 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
 // Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
 // as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
 // takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step, two
-// blocks an SM), the fold (0.4 a segment at d = 64, by d squared) and the second walk.  Taken when a
+// blocks an SM), the fold (0.5 a segment at d = 64) and the second walk.  Taken when a
 // tenth is gained.  Forward at bf16, without and with the segments that it takes: 1x4x16384x64 578 and
-// 135 us (10 segments), 1x8x4096x64 154 and 74, 2x16x4096x64 168 and 159; 4x16x4096x64 fills the
-// machine: 188 without, 254 with three.
+// 108 us, 1x8x4096x64 154 and 62, 2x16x4096x64 168 and 157; 4x16x4096x64 fills the machine: 188
+// without, 254 with three.
 Segments segments(const Problem& p) {
     constexpr int SMS = 148;
     const long long BH = static_cast<long long>(p.B) * p.H;
