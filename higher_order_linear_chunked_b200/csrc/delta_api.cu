@@ -18,7 +18,7 @@ bool width_ok(int d) { return d == 32 || d == 64 || d == 128; }
 hla_status_t check_shape(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {
     if (dtype != HLA_F32 && dtype != HLA_BF16) return HLA_ERR_DTYPE;
     if (B < 1 || Hk < 1 || H < 1 || T < 1 || d < 1 || dv < 1) return HLA_ERR_SHAPE;
-    if ((long long)B * H > 65535 || (long long)B * H * T >= (1LL << 31)) return HLA_ERR_SHAPE;
+    if ((long long)B * H > (1LL << 24) || (long long)B * H * T >= (1LL << 31)) return HLA_ERR_SHAPE;
     if (H % Hk != 0) return HLA_ERR_SHAPE;
     if (!width_ok(d) || !width_ok(dv)) return HLA_ERR_UNSUPPORTED;
     return HLA_OK;

@@ -17,16 +17,18 @@
  * uses query/key head h / (H / Hk).  States are [B][H][d][dv].  Base addresses are 16-byte
  * aligned (g, beta, lengths: 4-byte).
  *
- * Supported shapes.  d and dv each in {32, 64, 128}; T >= 1; B, Hk, H >= 1; B*H <= 65535,
+ * Supported shapes.  d and dv each in {32, 64, 128}; T >= 1; B, Hk, H >= 1; B*H <= 2^24,
  * B*H*T < 2^31.  Anything else returns HLA_ERR_UNSUPPORTED or HLA_ERR_SHAPE before any launch.
+ * Outputs must not overlap inputs or one another, except where a call says so.
  *
  * Padded batches.  lengths: NULL, or device int [B]; sequence b then has min(max(lengths[b], 0), T)
  * tokens.  What stands in the rows behind a sequence's end is not used (it may be NaN); the
  * outputs and gradients of those rows are written as zero, and the state is the one after the
  * last token (state_in itself where there is none).
  *
- * Values.  g may be any number up to where exp(g) overflows; g below -120 (-inf too) counts as
- * -120, whose exp is zero in fp32, and so starts the head anew at that token.
+ * Values.  g below -120 (-inf too) counts as -120, whose exp is zero in fp32, and so starts the head
+ * anew at that token.  Positive g are allowed while their sums over 64 neighbouring tokens stay below
+ * 88 (exp of it is the largest fp32); decays (g <= 0) always do.
  */
 #ifndef HLA_DELTA_H_
 #define HLA_DELTA_H_
@@ -73,7 +75,7 @@ hla_status_t hla_delta_step(float* state, const void* q, const void* k, const vo
  *     sums over its value heads.  dg, dbeta: like g.  Rows behind a sequence's end get zeros.
  *   dstate_out: [B][H][d][dv], or NULL for zeros.  dstate_in: the gradient at state_in, or NULL when
  *     it is not wanted.
- * The workspace holds about 1 kB a token and head at d = dv = 64 (bf16).  A fixed order of sums:
+ * The workspace holds about 1.6 kB a token and head at d = dv = 64 (bf16).  A fixed order of sums:
  * the same inputs give the same bits.
  */
 size_t hla_delta_backward_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv);
@@ -105,8 +107,7 @@ hla_status_t hla_group_norm_forward(const void* x, const void* gate, const float
 
 /* Gradients of sum(y * dy).  dgate: required with a gate (NULL without); dweight, dbias: fp32 [C],
  * each may be NULL when it is not wanted.  Workspace: hla_group_norm_backward_workspace_bytes()
- * (partial column sums; needed when dweight or dbias is wanted).  Sums are taken in a fixed order.
- * dx may be x or dy, dgate may be gate. */
+ * (partial column sums; needed when dweight or dbias is wanted).  Sums are taken in a fixed order. */
 size_t hla_group_norm_backward_workspace_bytes(hla_dtype_t dtype, long long rows, int C, int groups);
 hla_status_t hla_group_norm_backward(const void* x, const void* gate, const float* weight, const float* bias,
                                      const void* dy, void* dx, void* dgate, float* dweight, float* dbias,

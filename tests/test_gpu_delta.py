@@ -163,6 +163,34 @@ def test_many_heads():
     check(S, last, "state")
 
 
+def test_more_heads_than_a_grid_axis():
+    """70400 heads (a grid's second axis ends at 65535): every head's result, by a repeated batch."""
+    x = leaves("bf16", 4, 1, 64, 2, 32, 32, seed=31, state=True)
+    many = [t.repeat(275, *([1] * (t.dim() - 1))).to(DEV) for t in x]
+    o, S = hla.gated_delta(*many[:5], scale=0.5, initial_state=many[5], return_state=True)
+    want, last = od.forward(*x[:5], 0.5, x[5])
+    check(o[-4:], want, "o")
+    check(S[-4:], last, "state")
+    assert torch.equal(o.view(275, 4, 64, 2, 32), o[:4].expand(275, 4, 64, 2, 32))
+    assert torch.equal(S.view(275, 4, 64, 32, 32), S[:4].expand(275, 4, 64, 32, 32))
+    step = hla.gated_delta_step(many[5], *(t[:, :, 0].contiguous() for t in many[:5]), scale=0.5)
+    check(step[-4:], want[:, :, 0], "step")
+
+
+def test_nothing_beside_the_outputs_is_written():
+    """Outputs, state and workspace in the middle of larger buffers: the rest keeps its values."""
+    x = [t.to(DEV) for t in leaves("bf16", 2, 1, 2, 75, 64, 32, seed=32)[:5]]
+    n = hla.gated_delta_workspace_bytes(torch.bfloat16, 2, 1, 2, 75, 64, 32)
+    big = [torch.full((4, 2, 75, 32), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((4, 2, 64, 32), 7.0, device=DEV),
+           torch.full((n + 8192,), 7, dtype=torch.uint8, device=DEV)]
+    ref, last = hla.gated_delta(*x, return_state=True)
+    hla.gated_delta(*x, out=big[0][1:3], state_out=big[1][1:3], workspace=big[2][4096:4096 + n])
+    torch.cuda.synchronize()
+    assert torch.equal(big[0][1:3], ref) and torch.equal(big[1][1:3], last)
+    for t in (big[0][0], big[0][3], big[1][0], big[1][3], big[2][:4096], big[2][4096 + n:]):
+        assert bool((t == 7).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d,dv", [(32, 32), (64, 64), (128, 128), (64, 128), (128, 32)])
 @pytest.mark.parametrize("B,Hk,H", [(1, 1, 1), (5, 2, 6)])
@@ -259,6 +287,9 @@ def test_refusals():
         hla.gated_delta(q, k, v, g, beta, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(hla.HLAError):
         hla.gated_delta(q[..., :48].contiguous(), k[..., :48].contiguous(), v, g, beta)
+    odd = torch.zeros(v.numel() + 1, dtype=v.dtype, device=DEV)[1:].view_as(v)
+    with pytest.raises(hla.HLAError, match="ALIGN"):
+        hla.gated_delta(q, k, odd, g, beta)
     with pytest.raises(hla.HLAError, match="SHAPE"):
         hla.gated_delta(q[:, :, :0], k[:, :, :0], v[:, :, :0], g[:, :, :0], beta[:, :, :0])
     with pytest.raises(TypeError, match="float32 or bfloat16"):

@@ -192,6 +192,19 @@ def test_same_bits_graph_and_streams():
     assert torch.equal(o, hla.gated_delta(*dev[:5], initial_state=dev[5]))
 
 
+def test_nothing_beside_the_workspace_is_written():
+    x, dout, dstate = inputs("bf16", 2, 1, 2, 75, 64, 32, seed=33)
+    dev, do, ds = [t.to(DEV) for t in x], dout.to(DEV), dstate.to(DEV)
+    n = hla.gated_delta_backward_workspace_bytes(torch.bfloat16, 2, 1, 2, 75, 64, 32)
+    ws = torch.full((n + 8192,), 7, dtype=torch.uint8, device=DEV)
+    ref = hla.gated_delta_backward(*dev[:5], do, initial_state=dev[5], dstate=ds)
+    got = hla.gated_delta_backward(*dev[:5], do, initial_state=dev[5], dstate=ds, workspace=ws[4096:4096 + n])
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+    assert bool((ws[:4096] == 7).all()) and bool((ws[4096 + n:] == 7).all())
+
+
 def test_refusals():
     x, dout, dstate = inputs("bf16", 1, 2, 4, 8, 64, 64, seed=1)
     dev, do = [t.to(DEV) for t in x], dout.to(DEV)
