@@ -12,6 +12,7 @@ the current torch stream; arguments are checked here and again at the C boundary
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -57,6 +58,12 @@ def _library():
     return _bound
 
 
+@functools.lru_cache(maxsize=1024)
+def _bytes(query, *sizes) -> int:
+    """A workspace query's answer: sizes alone decide it."""
+    return int(getattr(_library(), query)(*sizes))
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -65,30 +72,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # both No
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-class _On:
-    """The device and stream of one call: the tensors' device is made current for it, and what the
-    call allocates is kept for the stream that uses it."""
+def _stream_of(device: int, stream) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
-    __slots__ = ("device", "given", "handle")
 
-    def __init__(self, device, stream):
-        self.device, self.given = device, stream
-        self.handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+def _keep(device: int, stream, *tensors) -> None:
+    """What a call allocated on the current stream is kept for the stream that uses it."""
+    if stream is not None and stream.cuda_stream != _raw_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
-    def keep(self, *tensors):
-        if self.given is not None and self.handle != _raw_stream(self.device.index):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.given)
 
-    def call(self, fn, what, *args):
-        if _current_device() == self.device.index:
+def _call(device: int, fn, what, *args) -> None:
+    """One library call with the tensors' device current."""
+    if _current_device() == device:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
             rc = fn(*args)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args)
-        if rc != HLA_OK:
-            raise HLAError(rc, what)
+    if rc != HLA_OK:
+        raise HLAError(rc, what)
 
 
 def _expect(name, t, shape, dtype, device):
@@ -154,7 +158,7 @@ def _lengths(lengths, B, device):
 
 def gated_delta_workspace_bytes(dtype, B: int, Hk: int, H: int, T: int, d: int, dv: int) -> int:
     """Bytes of workspace :func:`gated_delta` needs (0: no such call); ``dtype`` is torch's."""
-    return int(_library().hla_delta_workspace_bytes(_CODES.get(dtype, -1), B, Hk, H, T, d, dv))
+    return _bytes("hla_delta_workspace_bytes", _CODES.get(dtype, -1), B, Hk, H, T, d, dv)
 
 
 def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=None, lengths=None,
@@ -175,29 +179,29 @@ def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=N
     _lengths(lengths, B, dev)
     if initial_state is not None:
         _expect("initial_state", initial_state, (B, H, d, dv), torch.float32, dev)
-    on = _On(dev, stream)
+    on = q.get_device()
     lib = _library()
     if out is None:
         out = torch.empty_like(v)
-        on.keep(out)
+        _keep(on, stream, out)
     else:
         _expect("out", out, tuple(v.shape), v.dtype, dev)
     if state_out is not None:
         _expect("state_out", state_out, (B, H, d, dv), torch.float32, dev)
     elif return_state:
         state_out = torch.empty((B, H, d, dv), dtype=torch.float32, device=dev)
-        on.keep(state_out)
+        _keep(on, stream, state_out)
     code = _CODES[q.dtype]
     if workspace is None:
-        n = int(lib.hla_delta_workspace_bytes(code, B, Hk, H, T, d, dv))
+        n = _bytes("hla_delta_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        on.keep(workspace)
-    on.call(lib.hla_delta_forward, "hla_delta_forward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _keep(on, stream, workspace)
+    _call(on, lib.hla_delta_forward, "hla_delta_forward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), out.data_ptr(), _ptr(state_out), B, Hk,
             H, T, d, dv, code, LAYOUTS[layout], d ** -0.5 if scale is None else scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), on.handle)
+            workspace.numel() * workspace.element_size(), _stream_of(on, stream))
     return (out, state_out) if return_state else out
 
 
@@ -205,23 +209,25 @@ def gated_delta_step(state, q, k, v, g, beta, scale: Optional[float] = None, out
     """One token of every sequence: q, k [B, Hk, d], v [B, H, dv], g, beta [B, H]; advances
     ``state`` [B, H, d, dv] fp32 in place and returns o [B, H, dv] in v's type."""
     B, Hk, H, _, d, dv = _leaves(q, k, v, g, beta, None, step=True)
-    dev = q.device
-    _expect("state", state, (B, H, d, dv), torch.float32, dev)
-    on = _On(dev, stream)
+    on = q.get_device()
+    if not (state.shape == (B, H, d, dv) and state.dtype is torch.float32 and state.get_device() == on and
+            state.is_contiguous()):
+        _expect("state", state, (B, H, d, dv), torch.float32, q.device)
     if out is None:
         out = torch.empty_like(v)
-        on.keep(out)
+        if stream is not None:
+            _keep(on, stream, out)
     else:
-        _expect("out", out, tuple(v.shape), v.dtype, dev)
-    on.call(_library().hla_delta_step, "hla_delta_step rejected the call", state.data_ptr(), q.data_ptr(),
-            k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), B, Hk, H, d, dv,
-            _CODES[q.dtype], d ** -0.5 if scale is None else scale, on.handle)
+        _expect("out", out, tuple(v.shape), v.dtype, q.device)
+    _call(on, _library().hla_delta_step, "hla_delta_step rejected the call", state.data_ptr(), q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(), B, Hk, H, d, dv, _CODES[q.dtype],
+          d ** -0.5 if scale is None else scale, _stream_of(on, stream))
     return out
 
 
 def gated_delta_backward_workspace_bytes(dtype, B: int, Hk: int, H: int, T: int, d: int, dv: int) -> int:
     """Bytes of workspace :func:`gated_delta_backward` needs (0: no such call); ``dtype`` is torch's."""
-    return int(_library().hla_delta_backward_workspace_bytes(_CODES.get(dtype, -1), B, Hk, H, T, d, dv))
+    return _bytes("hla_delta_backward_workspace_bytes", _CODES.get(dtype, -1), B, Hk, H, T, d, dv)
 
 
 def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, initial_state=None, dstate=None,
@@ -238,22 +244,22 @@ def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, 
     for name, t in (("initial_state", initial_state), ("dstate", dstate)):
         if t is not None:
             _expect(name, t, (B, H, d, dv), torch.float32, dev)
-    on = _On(dev, stream)
+    on = q.get_device()
     lib = _library()
     code = _CODES[q.dtype]
     if workspace is None:
-        n = int(lib.hla_delta_backward_workspace_bytes(code, B, Hk, H, T, d, dv))
+        n = _bytes("hla_delta_backward_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     dq, dk, dvv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
     dstate0 = torch.empty_like(initial_state) if initial_state is not None else None
-    on.keep(dq, dk, dvv, dg, dbeta, dstate0, workspace)
-    on.call(lib.hla_delta_backward, "hla_delta_backward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _keep(on, stream, dq, dk, dvv, dg, dbeta, dstate0, workspace)
+    _call(on, lib.hla_delta_backward, "hla_delta_backward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), dout.data_ptr(), _ptr(dstate),
             dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dstate0), B, Hk, H, T, d,
             dv, code, LAYOUTS[layout], d ** -0.5 if scale is None else scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), on.handle)
+            workspace.numel() * workspace.element_size(), _stream_of(on, stream))
     return dq, dk, dvv, dg, dbeta, dstate0
 
 
@@ -273,10 +279,13 @@ def _norm_args(x, groups, weight, bias, gate, activation, center):
     C = x.shape[-1]
     if groups < 1 or C % groups:
         raise ValueError(f"{C} channels do not divide into {groups} groups")
-    if gate is not None:
+    on = x.get_device()
+    if gate is not None and not (gate.shape == x.shape and gate.dtype is x.dtype and gate.get_device() == on and
+                                 gate.is_contiguous()):
         _expect("gate", gate, tuple(x.shape), x.dtype, x.device)
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
+        if t is not None and not (t.shape == (C,) and t.dtype is torch.float32 and t.get_device() == on and
+                                  t.is_contiguous()):
             _expect(name, t, (C,), torch.float32, x.device)
     if x.numel() == 0:
         raise HLAError(2, f"x has no elements: {list(x.shape)}")
@@ -291,14 +300,16 @@ def group_norm(x, groups: int, weight=None, bias=None, gate=None, eps: float = 1
     with a gate shaped like x.  activation: "none" or "silu".  Returns y in x's type; ``out`` may be
     x or gate.  A row here is one position: nothing is shared between positions."""
     C, rows, flags = _norm_args(x, groups, weight, bias, gate, activation, center)
-    on = _On(x.device, stream)
+    on = x.get_device()
     if out is None:
         out = torch.empty_like(x)
-        on.keep(out)
+        if stream is not None:
+            _keep(on, stream, out)
     else:
         _expect("out", out, tuple(x.shape), x.dtype, x.device)
-    on.call(_library().hla_group_norm_forward, "hla_group_norm_forward rejected the call", x.data_ptr(), _ptr(gate),
-            _ptr(weight), _ptr(bias), out.data_ptr(), rows, C, groups, _CODES[x.dtype], eps, flags, on.handle)
+    _call(on, _library().hla_group_norm_forward, "hla_group_norm_forward rejected the call", x.data_ptr(), _ptr(gate),
+            _ptr(weight), _ptr(bias), out.data_ptr(), rows, C, groups, _CODES[x.dtype], eps, flags,
+          _stream_of(on, stream))
     return out
 
 
@@ -308,7 +319,7 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
     x's type, dweight and dbias fp32, each None where its input is None."""
     C, rows, flags = _norm_args(x, groups, weight, bias, gate, activation, center)
     _expect("dy", dy, tuple(x.shape), x.dtype, x.device)
-    on = _On(x.device, stream)
+    on = x.get_device()
     lib = _library()
     dx = torch.empty_like(x)
     dgate = torch.empty_like(gate) if gate is not None else None
@@ -317,13 +328,13 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
     nbytes = 0
     if weight is not None or bias is not None:
         if workspace is None:
-            n = int(lib.hla_group_norm_backward_workspace_bytes(_CODES[x.dtype], rows, C, groups))
+            n = _bytes("hla_group_norm_backward_workspace_bytes", _CODES[x.dtype], rows, C, groups)
             if n == 0:
                 raise HLAError(5, f"no group norm kernel for {rows} rows of {C} channels in {groups} groups")
             workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
         nbytes = workspace.numel() * workspace.element_size()
-    on.keep(dx, dgate, dweight, dbias, workspace)
-    on.call(lib.hla_group_norm_backward, "hla_group_norm_backward rejected the call", x.data_ptr(), _ptr(gate),
+    _keep(on, stream, dx, dgate, dweight, dbias, workspace)
+    _call(on, lib.hla_group_norm_backward, "hla_group_norm_backward rejected the call", x.data_ptr(), _ptr(gate),
             _ptr(weight), _ptr(bias), dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dweight), _ptr(dbias), rows, C,
-            groups, _CODES[x.dtype], eps, flags, _ptr(workspace), nbytes, on.handle)
+            groups, _CODES[x.dtype], eps, flags, _ptr(workspace), nbytes, _stream_of(on, stream))
     return dx, dgate, dweight, dbias
