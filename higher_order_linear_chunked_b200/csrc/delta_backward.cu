@@ -42,7 +42,9 @@ struct Rev {
     static constexpr int DK = DK_, CS = 16 * NG_;
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;
-    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2);   // as in the forward walk
+    // state warps of 16 columns, as in the forward walk, but four at d = 128: it has half again as many
+    // products between its exchanges (16 heads of 4096x128: four 246 us, two 256)
+    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2);
     // with one state warp a group, another one takes the outputs' share of dS, a chunk ahead of it
     static constexpr int W_SIDE = NH == 1 ? NG_ : 0;
     static constexpr int AHEAD = (BF ? 2 : 1) + (W_SIDE ? 1 : 0), NS = AHEAD + 1, NLD = BF ? 2 : 4;

@@ -52,9 +52,9 @@ struct Cfg {
     static constexpr int AHEAD = BF ? 2 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
     // state warps of 16 columns: one holds 64 keys' part of the state and the chunk's terms in its
-    // registers (bf16: 4x16x4096x64 the same with one and two, with half the warps); more keys, or the
-    // six products of fp32 terms, are worth the exchanges
-    static constexpr int NH = DK_ == 128 ? 4 : (BF || DK_ == 32 ? 1 : 2);
+    // registers (bf16: 4x16x4096x64 the same with one and two, with half the warps); twice the keys, or
+    // the six products of fp32 terms, are worth the exchanges (2x16x4096x128: two 234 us, four 240)
+    static constexpr int NH = DK_ == 128 || (!BF && DK_ == 64) ? 2 : 1;
     static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? NG_ : 0;
     static constexpr int WARPS = W_STATE + W_OUT + NLD;
     static constexpr int KTILE = KT * C * DK_ * 2;
