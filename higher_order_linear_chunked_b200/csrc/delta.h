@@ -30,23 +30,27 @@ cudaError_t forward(const Problem& p, void* ws, cudaStream_t st);
 size_t records_bytes(const Problem& p, bool gradients);
 cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st);
 
-// How a sequence is cut (delta_fold.cu): `count` segments of `chunks` chunks (1: not at all), and the
-// floats of the segments' summaries and of the states before them.
+// How a sequence is cut (delta_fold.cu), in a forward call or for the gradients' two walks: `count`
+// segments of `chunks` chunks (1: not at all), and the floats of the segments' summaries and of the
+// states before them.
 struct Segments {
     int count, chunks;
     size_t sums, starts;
 };
-Segments segments(const Problem& p);
+Segments segments(const Problem& p, bool gradients);
+// Value columns of a block of the gradients' two walks over `walked` heads (times segments).
+int gradient_columns(const Problem& p, long long walked);
 // The states between the segments, from the first on: sums [BH][count - 1][d][dv | d] holds (B | A) of
 // every segment but the last (the first one's B from the given state), first the given state or null.
 // With back: from the last on, S = A^T S' + back [BH][count][d][dv].  out: [BH][count][d][dv].
 cudaError_t fold(const Problem& p, const Segments& g, const float* sums, const float* back, const float* first,
                  float* out, cudaStream_t st);
 
-// The forward walk for the gradients: the state before each block of block_chunks chunks
-// [BH][blocks][d][dv] and each token's error R [BH][T][dv]; records in the gradients' form.  sums and
-// starts: segments(p)'s floats (sums is read again for the reverse walk).
-cudaError_t store_states(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states,
+// The forward walk for the gradients, with the records in their form: the segments' summaries (sums for
+// fold()); and the state before each block of block_chunks chunks [BH][blocks][d][dv] and each token's
+// error R [BH][T][dv], from the states before the segments (or before the first token: one segment).
+cudaError_t summarize(const Problem& p, const Segments& g, const uint8_t* records, float* sums, cudaStream_t st);
+cudaError_t store_states(const Problem& p, const Segments& g, const uint8_t* records, const float* first, float* states,
                          float* errors, int block_chunks, cudaStream_t st);
 
 // Gradients (delta_backward.cu).  dstate_out: the gradient at the last state, or null; dstate_in: the

@@ -69,7 +69,10 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
     constexpr int DK = F::DK, NH = F::NH, DH = DK / NH, TN = 4 / (NH == 1 ? 2 : NH), CS = F::CS, KT = F::KT;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // warp w runs on quarter w % 4 of an SM: the state warps on other quarters than the forward walk's
+    // state warps, beside which they run
+    const int warp = tid >> 5;
     const int slices = a.dv / CS, walked = F::SUMMARY ? a.segments - 1 : a.segments;
     const int col0 = (blockIdx.x % slices) * CS, bh = blockIdx.x / slices / walked;
     const int seg = (blockIdx.x / slices) % walked + (F::SUMMARY ? 1 : 0);
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
             for (int j = 0; j < 4; ++j)
                 to[static_cast<long long>(own_key + 8 * n + (j & 1)) * a.dv + own_col + 8 * (j >> 1)] = S[n][j];
     }
+    previous_done();
 }
 
 // ------------------------------------------------------------------ gradients of a block
@@ -1052,7 +1056,7 @@ Space space(const Problem& p) {
     s.H = s.R + rows;
     s.dq = s.H + rows;
     s.dk = s.dq + part;
-    const Segments g = segments(p);
+    const Segments g = segments(p, true);
     s.sums = s.dk + part;
     s.starts = s.sums + g.sums * 4;
     s.back = s.starts + g.starts * 4;
@@ -1066,28 +1070,42 @@ cudaError_t start(const ReverseArgs& a, int blocks, cudaStream_t st) {
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = allow_smem<k_delta_reverse<F>>(F::bytes);
     if (e != cudaSuccess) return e;
-    k_delta_reverse<F><<<blocks, F::WARPS * 32, F::bytes, st>>>(a);
-    return cudaGetLastError();
+    return launch_beside(k_delta_reverse<F>, blocks, F::WARPS * 32, F::bytes, st, a);
 }
 
-// The reverse walk; over segments with what lies behind each from a summary of the later ones (the
-// linear part of a segment backwards is the transpose of the forward walk's A).
+// The two walks.  Neither needs the other, so the reverse walk runs beside the forward one, and so do
+// their summaries and folds where there are segments (the linear part of a segment backwards is the
+// transpose of the forward walk's A).  4x16x4096x64 in bf16 222 us, one after the other 314; fp32
+// 2x8x4096x32 (in segments) all gradients 169 and 205, 2x16x512x32 50 and 68.
 template <typename E, int DK>
-cudaError_t reverse(const Problem& p, const Gradients& gr, char* ws, const Space& s, cudaStream_t st) {
+cudaError_t walks(const Problem& p, const Gradients& gr, char* ws, const Space& s, cudaStream_t st) {
     constexpr int NG = sizeof(E) == 2 ? 2 : 1;
-    const Segments g = segments(p);
+    const Segments g = segments(p, true);
     const int slices = p.dv / (16 * NG), BH = p.B * p.H;
+    const uint8_t* records = reinterpret_cast<uint8_t*>(ws + s.records);
+    const float* first = p.state_in;
     float* back = reinterpret_cast<float*>(ws + s.back);
     float* behind = reinterpret_cast<float*>(ws + s.behind);
     ReverseArgs a{p.q, p.k, gr.dout, reinterpret_cast<uint8_t*>(ws + s.records), gr.dstate_out, p.lengths, gr.dstate_in,
                   reinterpret_cast<float*>(ws + s.dstates), reinterpret_cast<float*>(ws + s.H), back,
                   p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, block_tokens(p) / C, g.count, g.chunks, p.scale};
+    cudaError_t e = cudaSuccess;
     if (g.count > 1) {
-        cudaError_t e = start<Rev<E, DK, NG, true>>(a, BH * (g.count - 1) * slices, st);
-        if (e == cudaSuccess) e = fold(p, g, reinterpret_cast<float*>(ws + s.sums), back, gr.dstate_out, behind, st);
-        if (e != cudaSuccess) return e;
+        float* sums = reinterpret_cast<float*>(ws + s.sums);
+        float* starts = reinterpret_cast<float*>(ws + s.starts);
+        e = summarize(p, g, records, sums, st);
+        if (e == cudaSuccess) e = start<Rev<E, DK, NG, true>>(a, BH * (g.count - 1) * slices, st);
+        if (e == cudaSuccess) e = fold(p, g, sums, nullptr, p.state_in, starts, st);
+        if (e == cudaSuccess) e = fold(p, g, sums, back, gr.dstate_out, behind, st);
         a.behind = behind;
+        first = starts;
     }
+    if (e == cudaSuccess)
+        e = store_states(p, g, records, first, reinterpret_cast<float*>(ws + s.states), reinterpret_cast<float*>(ws + s.R),
+                         block_tokens(p) / C, st);
+    if (e != cudaSuccess) return e;
+    if constexpr (sizeof(E) == 2 && DK <= 64)
+        if (gradient_columns(p, static_cast<long long>(p.B) * p.H * g.count) == 64) return start<Rev<E, DK, 4, false>>(a, BH * g.count * (p.dv / 64), st);
     return start<Rev<E, DK, NG, false>>(a, BH * g.count * slices, st);
 }
 
@@ -1114,10 +1132,7 @@ cudaError_t all(const Problem& p, const Gradients& gr, char* ws, cudaStream_t st
     const Space s = space(p);
     uint8_t* records = reinterpret_cast<uint8_t*>(ws + s.records);
     cudaError_t e = prepare(p, true, records, st);
-    if (e == cudaSuccess)
-        e = store_states(p, records, reinterpret_cast<float*>(ws + s.sums), reinterpret_cast<float*>(ws + s.starts),
-                         reinterpret_cast<float*>(ws + s.states), reinterpret_cast<float*>(ws + s.R), block_tokens(p) / C, st);
-    if (e == cudaSuccess) e = reverse<E, DK>(p, gr, ws, s, st);
+    if (e == cudaSuccess) e = walks<E, DK>(p, gr, ws, s, st);
     if (e == cudaSuccess) {
         if (p.dv == 32) e = block_grads<E, DK, 32>(p, gr, ws, s, st);
         else if (p.dv == 64) e = block_grads<E, DK, 64>(p, gr, ws, s, st);
@@ -1137,7 +1152,7 @@ cudaError_t all(const Problem& p, const Gradients& gr, char* ws, cudaStream_t st
 }  // namespace
 
 size_t backward_bytes(const Problem& p) { return space(p).end; }
-int backward_launches(const Problem& p) { return (p.H != p.Hk ? 5 : 4) + (segments(p).count > 1 ? 4 : 0); }
+int backward_launches(const Problem& p) { return (p.H != p.Hk ? 5 : 4) + (segments(p, true).count > 1 ? 4 : 0); }
 
 cudaError_t backward(const Problem& p, const Gradients& gr, void* ws, cudaStream_t st) {
     char* w = static_cast<char*>(ws);

@@ -5,6 +5,8 @@ namespace hla {
 namespace delta {
 namespace {
 
+constexpr int kSMs = 148;
+
 struct FoldArgs {
     const float *sums, *back, *first;
     float* out;
@@ -50,6 +52,7 @@ __global__ void __launch_bounds__(DK * 2) k_delta_fold(const FoldArgs a) {
         }
         cp_commit();
     };
+    next_may_start();                    // REV runs beside the fold from the first segment on
     ask(1);
     ask(2);
     float cur[4] = {};
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(DK * 2) k_delta_fold(const FoldArgs a) {
         put(s0 + (n + 1) * step, cur);
     }
     cp_wait<0>();
+    if (REV) previous_done();
 }
 
 template <int DK, bool REV>
@@ -98,11 +102,23 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
     static_assert(bytes <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = allow_smem<k_delta_fold<DK, REV>>(bytes);
     if (e != cudaSuccess) return e;
-    k_delta_fold<DK, REV><<<p.B * p.H * (p.dv / 8), DK * 2, bytes, st>>>(a);
+    const int blocks = p.B * p.H * (p.dv / 8);
+    if (REV) return launch_beside(k_delta_fold<DK, REV>, blocks, DK * 2, bytes, st, a);
+    k_delta_fold<DK, REV><<<blocks, DK * 2, bytes, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+// A block of one walk beside a block of the other on an SM costs both as much as one after the other,
+// a block of twice the columns only a quarter more: 64 columns where both walks' blocks then have an SM
+// each and blocks of 32 would not.  4x16x4096x64: the walks one after the other 314 us, side by side 342
+// with 32 columns and 222 with 64.
+int gradient_columns(const Problem& p, long long walked) {
+    if (!p.bf16) return 16;
+    const long long walks = 2 * walked;
+    return p.d <= 64 && p.dv % 64 == 0 && walks * (p.dv / 32) > kSMs && walks * (p.dv / 64) <= kSMs ? 64 : 32;
+}
 
 // Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
 // as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
@@ -111,22 +127,32 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
 // tenth is gained.  Forward at bf16, without and with the segments that it takes: 1x4x16384x64 578 and
 // 108 us, 1x8x4096x64 154 and 62, 2x16x4096x64 168 and 157; 4x16x4096x64 fills the machine: 188
 // without, 254 with three.
-Segments segments(const Problem& p) {
-    constexpr int SMS = 148;
+// The gradients have two such walks side by side, a reverse step 1.3; on SMs of their own that is all,
+// with 64 columns a block 1.25 times it, on shared ones 1.35 a wave (between 1.2 and 1.75 eight shapes
+// of ten chose the same, the two others best here): 2x16x4096x64 needs no segments, 371 us with the rest of
+// the gradients, not 424.
+Segments segments(const Problem& p, bool gradients) {
     const long long BH = static_cast<long long>(p.B) * p.H;
     const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16, fit = p.bf16 ? (p.d <= 64 ? 2 : 1) : (p.d == 32 ? 2 : 1);
     const auto waves = [&](long long blocks, int fit) {
-        const long long rest = blocks % (SMS * fit);
-        return (fit == 2 ? 1.25 : 1.0) * static_cast<double>(blocks / (SMS * fit)) + (rest == 0 ? 0.0 : rest <= SMS ? 1.0 : 1.25);
+        const long long rest = blocks % (kSMs * fit);
+        return (fit == 2 ? 1.25 : 1.0) * static_cast<double>(blocks / (kSMs * fit)) + (rest == 0 ? 0.0 : rest <= kSMs ? 1.0 : 1.25);
+    };
+    const auto walk_waves = [&](long long blocks) {
+        if (!gradients) return waves(blocks, fit);
+        if (2 * blocks <= kSMs) return 1.3;
+        if (gradient_columns(p, blocks * CS / p.dv) == 64) return 1.3 * 1.25;
+        return 1.3 * 1.35 * waves(blocks, fit);
     };
     const double fold_step = 0.4 * (p.d / 64.0) * (p.d / 64.0) + 0.1;
     int best = 1;
-    double cost = 0.9 * waves(BH * p.dv / CS, fit) * NC;
+    double cost = 0.9 * walk_waves(BH * p.dv / CS) * NC;
     for (int n = 2; n <= 64 && n <= NC / 4; ++n) {
         const int chunks = (NC + n - 1) / n;
         if ((NC + chunks - 1) / chunks != n) continue;
         const long long summaries = BH * (static_cast<long long>(n - 2) * (p.dv + p.d) + p.dv) / CS;
-        const double c = 0.85 * chunks * waves(summaries, 2) + fold_step * n + 8 + chunks * waves(BH * n * p.dv / CS, fit);
+        const double c = 0.85 * chunks * waves(summaries, 2) * (gradients ? 1.5 : 1.0) + fold_step * n + 8 +
+                         chunks * walk_waves(BH * n * p.dv / CS);
         if (c < cost) cost = c, best = n;
     }
     Segments g{best, (NC + best - 1) / best, 0, 0};

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
     const int slices = MODE == SUMMARY ? vslices + DK / CS : vslices;
     const int walked = MODE == SUMMARY ? a.segments - 1 : a.segments;
     const int slice = blockIdx.x % slices, seg = (blockIdx.x / slices) % walked, bh = blockIdx.x / slices / walked;
+    next_may_start();
     const bool unit = MODE == SUMMARY && slice >= vslices;      // columns of the transition: v = 0, S = I
     const int col0 = (unit ? slice - vslices : slice) * CS;
     if (unit && seg == 0) return;                               // the first segment starts from the given state
@@ -536,16 +537,13 @@ cudaError_t start(const WalkArgs& a, int blocks, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// The states before the segments: the segments' summaries, then one after another.
 template <typename E, int DK, bool GR>
-cudaError_t states_between(const Problem& p, const Segments& g, const uint8_t* records, float* sums, float* starts,
-                           cudaStream_t st) {
+cudaError_t summaries(const Problem& p, const Segments& g, const uint8_t* records, float* sums, cudaStream_t st) {
     using F = Cfg<E, DK, sizeof(E) == 2 ? 2 : 1, SUMMARY, GR>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const WalkArgs a{p.q, p.k, p.v, records, p.state_in, p.lengths, nullptr, nullptr, sums, nullptr, nullptr, 1,
                      p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
-    const cudaError_t e = start<F>(a, p.B * p.H * (g.count - 1) * ((p.dv + DK) / F::CS), st);
-    return e == cudaSuccess ? fold(p, g, sums, nullptr, p.state_in, starts, st) : e;
+    return start<F>(a, p.B * p.H * (g.count - 1) * ((p.dv + DK) / F::CS), st);
 }
 
 template <typename E, int DK>
@@ -556,52 +554,63 @@ cudaError_t walk(const Problem& p, void* ws, cudaStream_t st) {
     const int BH = p.B * p.H;
     char* w = static_cast<char*>(ws);
     uint8_t* records = reinterpret_cast<uint8_t*>(w);
-    const Segments g = segments(p);
+    const Segments g = segments(p, false);
     float* sums = reinterpret_cast<float*>(w + records_bytes(p, false));
     float* starts = sums + g.sums;
     cudaError_t e = prepare(p, false, records, st);
-    if (e == cudaSuccess && g.count > 1) e = states_between<E, DK, false>(p, g, records, sums, starts, st);
+    if (e == cudaSuccess && g.count > 1) e = summaries<E, DK, false>(p, g, records, sums, st);
+    if (e == cudaSuccess && g.count > 1) e = fold(p, g, sums, nullptr, p.state_in, starts, st);
     if (e != cudaSuccess) return e;
     WalkArgs a{p.q, p.k, p.v, records, g.count > 1 ? starts : p.state_in, p.lengths, p.o, p.state_out, nullptr, nullptr,
                nullptr, 1, p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
     return start<F>(a, BH * g.count * (p.dv / F::CS), st);
 }
 
-template <typename E, int DK>
-cudaError_t walk_store(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states, float* errors,
-                       int block_chunks, cudaStream_t st) {
-    constexpr int NG = sizeof(E) == 2 ? 2 : 1;
+template <typename E, int DK, int NG>
+cudaError_t walk_store(const Problem& p, const Segments& g, const uint8_t* records, const float* first, float* states,
+                       float* errors, int block_chunks, cudaStream_t st) {
     using F = Cfg<E, DK, NG, STORE, true>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
-    const Segments g = segments(p);
-    if (g.count > 1) {
-        const cudaError_t e = states_between<E, DK, true>(p, g, records, sums, starts, st);
-        if (e != cudaSuccess) return e;
-    }
-    WalkArgs a{p.q, p.k, p.v, records, g.count > 1 ? starts : p.state_in, p.lengths, nullptr, nullptr, nullptr, states,
+    WalkArgs a{p.q, p.k, p.v, records, first, p.lengths, nullptr, nullptr, nullptr, states,
                errors, block_chunks, p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, g.count, g.chunks, p.scale};
     return start<F>(a, p.B * p.H * g.count * (p.dv / F::CS), st);
 }
 
 }  // namespace
 
-cudaError_t store_states(const Problem& p, const uint8_t* records, float* sums, float* starts, float* states,
+cudaError_t summarize(const Problem& p, const Segments& g, const uint8_t* records, float* sums, cudaStream_t st) {
+    if (p.bf16) {
+        if (p.d == 32) return summaries<bf16, 32, true>(p, g, records, sums, st);
+        if (p.d == 64) return summaries<bf16, 64, true>(p, g, records, sums, st);
+        return summaries<bf16, 128, true>(p, g, records, sums, st);
+    }
+    if (p.d == 32) return summaries<float, 32, true>(p, g, records, sums, st);
+    if (p.d == 64) return summaries<float, 64, true>(p, g, records, sums, st);
+    return summaries<float, 128, true>(p, g, records, sums, st);
+}
+
+cudaError_t store_states(const Problem& p, const Segments& g, const uint8_t* records, const float* first, float* states,
                          float* errors, int block_chunks, cudaStream_t st) {
     if (p.bf16) {
-        if (p.d == 32) return walk_store<bf16, 32>(p, records, sums, starts, states, errors, block_chunks, st);
-        if (p.d == 64) return walk_store<bf16, 64>(p, records, sums, starts, states, errors, block_chunks, st);
-        return walk_store<bf16, 128>(p, records, sums, starts, states, errors, block_chunks, st);
+        const bool wide = gradient_columns(p, static_cast<long long>(p.B) * p.H * g.count) == 64;
+        if (p.d == 32)
+            return wide ? walk_store<bf16, 32, 4>(p, g, records, first, states, errors, block_chunks, st)
+                        : walk_store<bf16, 32, 2>(p, g, records, first, states, errors, block_chunks, st);
+        if (p.d == 64)
+            return wide ? walk_store<bf16, 64, 4>(p, g, records, first, states, errors, block_chunks, st)
+                        : walk_store<bf16, 64, 2>(p, g, records, first, states, errors, block_chunks, st);
+        return walk_store<bf16, 128, 2>(p, g, records, first, states, errors, block_chunks, st);
     }
-    if (p.d == 32) return walk_store<float, 32>(p, records, sums, starts, states, errors, block_chunks, st);
-    if (p.d == 64) return walk_store<float, 64>(p, records, sums, starts, states, errors, block_chunks, st);
-    return walk_store<float, 128>(p, records, sums, starts, states, errors, block_chunks, st);
+    if (p.d == 32) return walk_store<float, 32, 1>(p, g, records, first, states, errors, block_chunks, st);
+    if (p.d == 64) return walk_store<float, 64, 1>(p, g, records, first, states, errors, block_chunks, st);
+    return walk_store<float, 128, 1>(p, g, records, first, states, errors, block_chunks, st);
 }
 
 size_t forward_bytes(const Problem& p) {
-    const Segments g = segments(p);
+    const Segments g = segments(p, false);
     return records_bytes(p, false) + sizeof(float) * (g.sums + g.starts);
 }
-int forward_launches(const Problem& p) { return segments(p).count > 1 ? 4 : 2; }
+int forward_launches(const Problem& p) { return segments(p, false).count > 1 ? 4 : 2; }
 
 cudaError_t forward(const Problem& p, void* ws, cudaStream_t st) {
     if (p.bf16) {

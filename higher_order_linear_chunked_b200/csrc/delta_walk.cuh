@@ -10,7 +10,9 @@
 namespace hla {
 namespace delta {
 
-// Dynamic shared memory of a kernel, asked for once a device (the attribute stays with the device).
+// Dynamic shared memory of a kernel, asked for once a device (the attribute stays with the device), and
+// all of an SM's memory as shared memory: blocks of another kernel fit beside this one's only where the
+// split between shared memory and cache leaves them room, and the split of a busy SM stays as it is.
 template <auto KERNEL>
 inline cudaError_t allow_smem(int bytes) {
     static std::atomic<unsigned long long> done{0};
@@ -20,8 +22,32 @@ inline cudaError_t allow_smem(int bytes) {
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
     e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
+}
+
+// Two kernels that do not need one another run side by side: the second one is a programmatic dependent
+// of the first, launched once every block of the first has passed next_may_start(), and waits for the
+// first one's end at its own (previous_done()), so that whatever follows finds both complete.  What the
+// first one follows is an ordinary dependency of the first, complete before any of its blocks starts.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename A, typename... Args>
+inline cudaError_t launch_beside(void (*kernel)(A, Args...), int blocks, int threads, int smem, cudaStream_t st, A a, Args... more) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
 constexpr int kMS = 36;                      // floats of a row of the transposed system

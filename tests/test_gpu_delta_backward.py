@@ -144,6 +144,20 @@ def test_segments_of_a_padded_batch(dtype, d, dv):
     compare(x, dout, dstate, 0.2, lens)
 
 
+@pytest.mark.parametrize("d,dv,B,Hk,H,T,layout", [(64, 64, 6, 4, 8, 150, "bhtd"), (32, 64, 6, 8, 8, 97, "bthd"),
+                                                  (64, 128, 5, 2, 6, 70, "bthd")])
+def test_walks_side_by_side_in_wide_blocks(d, dv, B, Hk, H, T, layout):
+    """So many heads that narrow blocks of the two walks would share SMs, and wide ones do not."""
+    lens = torch.tensor([T, 0, 33, 64, 1, T + 5][:B], dtype=torch.int32)
+    x, dout, dstate = inputs("bf16", B, Hk, H, T, d, dv, seed=21)
+    for b, n in enumerate(lens.tolist()):
+        for t in (*x[:5], dout):
+            t[b, :, n:] = 0.0
+    compare(x, dout, dstate, 0.2, lens, layout)
+    one, two = run(x, dout, dstate, 0.2, lens, layout), run(x, dout, dstate, 0.2, lens, layout)
+    assert all(torch.equal(one[n], two[n]) for n in one)
+
+
 def test_against_differences():
     """fp32: the slope of the GPU forward along a direction, by a central difference.  The loss's own
     rounding (2^-24 of its terms' sizes, about 1e-6 of the loss's scale) over the step of 1e-2, and the
