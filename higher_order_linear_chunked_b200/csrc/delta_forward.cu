@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
     const int slices = MODE == SUMMARY ? vslices + DK / CS : vslices;
     const int walked = MODE == SUMMARY ? a.segments - 1 : a.segments;
     const int slice = blockIdx.x % slices, seg = (blockIdx.x / slices) % walked, bh = blockIdx.x / slices / walked;
-    next_may_start();
+    if (MODE != OUT) next_may_start();                          // the reverse walk of the same kind, if there is one
     const bool unit = MODE == SUMMARY && slice >= vslices;      // columns of the transition: v = 0, S = I
     const int col0 = (unit ? slice - vslices : slice) * CS;
     if (unit && seg == 0) return;                               // the first segment starts from the given state

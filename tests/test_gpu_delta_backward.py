@@ -158,6 +158,32 @@ def test_walks_side_by_side_in_wide_blocks(d, dv, B, Hk, H, T, layout):
     assert all(torch.equal(one[n], two[n]) for n in one)
 
 
+@pytest.mark.parametrize("dtype,B,H,T,d", [("bf16", 6, 8, 100, 64), ("bf16", 1, 2, 1500, 64), ("f32", 1, 2, 1500, 32),
+                                           ("f32", 9, 16, 70, 64)])
+def test_walks_side_by_side_in_a_graph(dtype, B, H, T, d):
+    """Every replay waits for both walks: new inputs in the captured buffers, the same bits as eager calls."""
+    x, dout, dstate = inputs(dtype, B, H, H, T, d, d, seed=22)
+    held = [t.to(DEV) for t in (*x[:5], dout, x[5], dstate)]
+
+    def call():
+        return hla.gated_delta_backward(*held[:6], scale=0.2, initial_state=held[6], dstate=held[7])
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for seed in (23, 24):
+        y, dy, ds = inputs(dtype, B, H, H, T, d, d, seed=seed)
+        for to, t in zip(held, (*y[:5], dy, y[5], ds)):
+            to.copy_(t)
+        for _ in range(3):
+            graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_against_differences():
     """fp32: the slope of the GPU forward along a direction, by a central difference.  The loss's own
     rounding (2^-24 of its terms' sizes, about 1e-6 of the loss's scale) over the step of 1e-2, and the
