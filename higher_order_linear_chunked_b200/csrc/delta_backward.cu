@@ -6,7 +6,7 @@
 //     Z  = diag(beta) H                        (the gradient at R, and at V)
 // the gradient at the state before the chunk is
 //     dS0 = e^(c_C) dS + (scale e^c Q)^T dO - (e^c K)^T Z.
-// Three passes: the forward walk again, which keeps the states before blocks of chunks and R; this
+// Three passes: the forward walk again, which keeps the states before blocks of chunks and R; beside it this
 // reverse walk, which keeps dS behind the blocks and H; and one kernel over all blocks, which has
 // then everything for dq, dk, dv, dbeta and dg.  R and H are per token, not per chunk (R is a token's
 // error, H the gradient at what it writes), so the blocks need not be the walks' chunks.
