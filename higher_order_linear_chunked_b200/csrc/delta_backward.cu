@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
         step_end();
     } else if (chunks > 0) {
         const int lt = (warp - w_load) * 32 + lane;
-        constexpr int LT = F::NLD * 32, REC = record_bytes(2, 3);
+        constexpr int LT = F::NLD * 32, REC = record_bytes(2);
         const long long ks = static_cast<long long>(kstep) * DK, vs = static_cast<long long>(vstep) * a.dv;
         const E* kp = static_cast<const E*>(a.k) + row_of(a.bthd, b, hk, a.Hk, 0, a.T) * DK;
         const E* qp = static_cast<const E*>(a.q) + row_of(a.bthd, b, hk, a.Hk, 0, a.T) * DK;

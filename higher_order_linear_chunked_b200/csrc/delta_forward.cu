@@ -46,9 +46,10 @@ struct Cfg {
     static constexpr Mode MODE = MODE_;
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;             // terms of q, k
-    static constexpr int OT = BF ? 2 : 3;             // terms of S0, U and P in the outputs: twice the
-                                                      // 8 bits that a bf16 output keeps
-    static constexpr int INV = GR ? 2 : 1, PT = GR ? 3 : OT;
+    // terms of S0, U and P in the outputs: fp32's 24 bits for either type, since an output may be far
+    // smaller than its terms (two terms, 16 bits, measured 184 us and not 194 for 4x16x4096x64 bf16)
+    static constexpr int OT = 3;
+    static constexpr int INV = GR ? 2 : 1;
     static constexpr int AHEAD = BF ? 2 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
     // state warps of 16 columns: one holds 64 keys' part of the state and the chunk's terms in its
@@ -62,14 +63,15 @@ struct Cfg {
     static constexpr int NS = AHEAD + 1;
     static constexpr int k = 0, x = k + KTILE, v = x + kXBytes;
     static constexpr int STAGE = (v + cols_bytes<E, CS>() + 255) / 256 * 256;
-    // ring of AHEAD + 2: gates, and for the outputs, a chunk behind, queries and P
-    static constexpr int NO = AHEAD + 2;
-    static constexpr int PB = PT * C * C * 2;
-    static constexpr int behind = NS * STAGE;
-    static constexpr int gates = 0, q = 512, p = q + KTILE;
-    static constexpr int OSTAGE = MODE_ == OUT ? p + PB : 512;
+    // ring of AHEAD + 2: gates, which the outputs need a chunk behind the state
+    static constexpr int NG_STAGES = AHEAD + 2;
+    static constexpr int gates = NS * STAGE;
+    // ring of AHEAD + 1: for the outputs, queries and P, asked for a chunk behind the rest
+    static constexpr int behind = gates + NG_STAGES * 512;
+    static constexpr int q = 0, p = q + KTILE;
+    static constexpr int OSTAGE = MODE_ == OUT ? p + kXBytes : 0;
     // S0 and U of the last two chunks for the outputs, the partial sums
-    static constexpr int sf = behind + NO * OSTAGE;
+    static constexpr int sf = behind + NS * OSTAGE;
     static constexpr int SB = NG_ * (DK_ / 16) * OT * 512;
     static constexpr int uf = sf + (MODE_ == OUT ? 2 * SB : 0);
     static constexpr int UB = NG_ * 2 * OT * 512;
@@ -139,11 +141,11 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         float4* const ex = reinterpret_cast<float4*>(sm + F::ex) + grp * NH * 128 + lane;
         uint8_t* const yf = sm + F::yf + grp * F::YB;
         uint8_t* const vf = reinterpret_cast<uint8_t*>(ex - lane);
-        int stage = 0, ostage = 0;
+        int stage = 0, gstage = 0;
         for (int s = -F::AHEAD; s < 0; ++s) step_end();
         for (int c = 0; c < chunks; ++c) {
             const uint32_t so = stage * F::STAGE;
-            const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + ostage * F::OSTAGE + F::gates);
+            const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates + gstage * 512);
             uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 16) + part * (DH / 16)) * OT * 32 + lane;
             uint2* uf = reinterpret_cast<uint2*>(sm + F::uf + (c & 1) * F::UB) + grp * 2 * OT * 64 + lane * 2;
             if (MODE == STORE) {
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
             }
             }
             if (++stage == F::NS) stage = 0;
-            if (++ostage == F::NO) ostage = 0;
+            if (++gstage == F::NG_STAGES) gstage = 0;
             step_end();
         }
         step_end();
@@ -409,11 +411,11 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         const uint32_t p_a = at_rows_first<C * 2>(sb + F::behind + F::p, 0, 0, lane);
         E* o = static_cast<E*>(a.o) + (vrow + static_cast<long long>(lane >> 2) * vstep) * a.dv + col0 + 16 * g + 2 * (lane & 3);
         const long long next8 = static_cast<long long>(8) * vstep * a.dv;
-        int ostage = 0;
+        int ostage = 0, gstage = 0;
         for (int s = -F::AHEAD; s < 1; ++s) step_end();
         for (int c = 0; c < chunks; ++c) {
             const uint32_t so = ostage * F::OSTAGE;
-            const Gates* G = reinterpret_cast<const Gates*>(sm + F::behind + so + F::gates);
+            const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates + gstage * 512);
             const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 16) * OT * 32 + lane;
             const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + (c & 1) * F::UB) + g * 2 * OT * 32 + lane;
             float acc[2][2][4] = {};          // [16 tokens][8 columns]
@@ -468,7 +470,8 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 }
             }
             o += 4 * next8;
-            if (++ostage == F::NO) ostage = 0;
+            if (++ostage == F::NS) ostage = 0;
+            if (++gstage == F::NG_STAGES) gstage = 0;
             step_end();
         }
     } else if (chunks > 0) {
@@ -479,23 +482,28 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         const E* kp = static_cast<const E*>(a.k) + krow * DK;
         const E* qp = static_cast<const E*>(a.q) + krow * DK;
         const E* vp = static_cast<const E*>(a.v) + vrow * a.dv + col0;
-        const uint8_t* rec = a.records + (static_cast<long long>(bh) * ((a.T + C - 1) / C) + t_first / C) *
-                                             record_bytes(F::INV, F::PT);
-        int stage = 0, ostage = 0;
+        constexpr int REC = record_bytes(F::INV);
+        const uint8_t* rec = a.records + (static_cast<long long>(bh) * ((a.T + C - 1) / C) + t_first / C) * REC;
+        int stage = 0, ostage = 0, gstage = 0;
         for (int c = 0; c <= chunks + F::AHEAD; ++c) {
+            if (MODE == OUT && c > 0 && c <= chunks) {      // queries and P of the chunk before
+                const uint32_t so = sb + F::behind + ostage * F::OSTAGE;
+                load_bytes<kXBytes, LT>(so + F::p, rec - REC + F::INV * kXBytes, lt);
+                load_tile<DK, KT, LT>(so + F::q, qp, ks, min(C, t_end - t_first - (c - 1) * C), lt);
+                qp += C * ks;
+                if (++ostage == F::NS) ostage = 0;
+            }
             if (c < chunks) {
-                const uint32_t sg = sb + stage * F::STAGE, so = sb + F::behind + ostage * F::OSTAGE;
+                const uint32_t sg = sb + stage * F::STAGE;
                 const int rows = min(C, t_end - t_first - c * C);
                 load_bytes<kXBytes, LT>(sg + F::x, rec, lt);
-                if (MODE == OUT) load_bytes<F::PB, LT>(so + F::p, rec + F::INV * kXBytes, lt);
-                load_bytes<512, LT>(so + F::gates, rec + F::INV * kXBytes + F::PB, lt);
+                load_bytes<512, LT>(sb + F::gates + gstage * 512, rec + (F::INV + 1) * kXBytes, lt);
                 if (!unit) load_cols<CS, LT>(sg + F::v, vp, vs, rows, lt);
                 load_tile<DK, KT, LT>(sg + F::k, kp, ks, rows, lt);
-                if (MODE == OUT) load_tile<DK, KT, LT>(so + F::q, qp, ks, rows, lt);
-                kp += C * ks; qp += C * ks; vp += C * vs;
-                rec += record_bytes(F::INV, F::PT);
+                kp += C * ks; vp += C * vs;
+                rec += REC;
                 if (++stage == F::NS) stage = 0;
-                if (++ostage == F::NO) ostage = 0;
+                if (++gstage == F::NG_STAGES) gstage = 0;
             }
             cp_commit();
             cp_wait<F::AHEAD - 1>();

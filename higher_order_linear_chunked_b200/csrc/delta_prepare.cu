@@ -22,23 +22,23 @@ struct PrepArgs {
     float scale;
 };
 
-template <typename E, int DK_, int PT_, int INV_>
+template <typename E, int DK_, int INV_>
 struct Prep {
     using Elem = E;
-    static constexpr int DK = DK_, PT = PT_, INV = INV_, KT = sizeof(E) == 2 ? 1 : 3;
+    static constexpr int DK = DK_, INV = INV_, KT = sizeof(E) == 2 ? 1 : 3;
     static constexpr int TILE = KT * C * DK * 2;
-    static constexpr int REC = record_bytes(INV, PT);
+    static constexpr int REC = record_bytes(INV);
     static constexpr int WARPS = INV == 1 ? 2 : 1;
     // shared memory: with one warp the inverses take the queries' place once P is there
     static constexpr int k = 0, q = k + TILE, x = WARPS == 2 ? q + TILE : q;
     static constexpr int m = WARPS == 2 ? x + kXBytes : q + (TILE > kXBytes ? TILE : kXBytes), p = m + C * kMS * 4;
-    static constexpr int TAIL = PT * C * C * 2 + 512, sum = p + TAIL;
+    static constexpr int TAIL = kXBytes + 512, sum = p + TAIL;
     static constexpr int bytes = sum + C * 8;
 };
 
-// The blocks above the diagonal of `terms` images, which the products do not write: by one warp.
-__device__ __forceinline__ void clear_above(uint8_t* to, int terms, int lane) {
-    for (int t = 0; t < terms; ++t)
+// The blocks above the diagonal of three terms' images, which the products do not write: by one warp.
+__device__ __forceinline__ void clear_above(uint8_t* to, int lane) {
+    for (int t = 0; t < 3; ++t)
         *reinterpret_cast<uint4*>(to + t * (C * C * 2) + piece<C * 2>(lane & 15, 2 + (lane >> 4))) = make_uint4(0u, 0u, 0u, 0u);
 }
 template <int N>
@@ -50,7 +50,7 @@ __device__ __forceinline__ void copy_out(uint8_t* to, const uint8_t* from, int l
 template <typename F>
 __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs a) {
     using E = typename F::Elem;
-    constexpr int DK = F::DK, KT = F::KT, PT = F::PT;
+    constexpr int DK = F::DK, KT = F::KT;
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
     load_tile<DK, KT, F::WARPS * 32>(sb + F::q, static_cast<const E*>(a.q) + kr * DK, ks, rows, tid);
     cp_commit();
     uint8_t* const pt = sm + F::p;
-    Gates* const gates = reinterpret_cast<Gates*>(pt + PT * C * C * 2);
+    Gates* const gates = reinterpret_cast<Gates*>(pt + kXBytes);
     float2* const sum = reinterpret_cast<float2*>(sm + F::sum);
     uint8_t* const rec = a.records + static_cast<long long>(blockIdx.x) * F::REC;
     float* const mt = reinterpret_cast<float*>(sm + F::m);
@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
         const float g = on ? a.g[vr + static_cast<long long>(lane) * vstep] : 0.f;
         const float beta = on ? a.beta[vr + static_cast<long long>(lane) * vstep] : 0.f;
         finish_gates(gates, sum, g, beta, lane);
-        clear_above(pt, PT, lane);
+        clear_above(pt, lane);
     }
-    if (F::WARPS == 2 && warp == 1) clear_above(xt, 3, lane);
+    if (F::WARPS == 2 && warp == 1) clear_above(xt, lane);
     cp_wait<0>();
     __syncthreads();
     // queries with keys for P, keys with keys for X, then for X'
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
     for (int part = first; part < end; ++part) {
 #pragma unroll 1
         for (int w = 0; w < 2; ++w)
-            products<DK, KT, PT>(part > 0, part == 2, sb + F::k, sb + (part > 0 ? F::k : F::q), sum, gates->beta, mt, pt,
+            products<DK, KT>(part > 0, part == 2, sb + F::k, sb + (part > 0 ? F::k : F::q), sum, gates->beta, mt, pt,
                                  a.scale, w, lane);
         __syncwarp();
         if (part > 0) {
@@ -96,14 +96,14 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
             __syncwarp();
         } else {
             copy_out<F::TAIL>(rec + F::INV * kXBytes, pt, lane);
-            if (F::WARPS == 1) clear_above(xt, 3, lane);                // the queries are done with
+            if (F::WARPS == 1) clear_above(xt, lane);                   // the queries are done with
         }
     }
 }
 
-template <typename E, int DK, int PT, int INV>
+template <typename E, int DK, int INV>
 cudaError_t launch(const Problem& p, uint8_t* records, cudaStream_t st) {
-    using F = Prep<E, DK, PT, INV>;
+    using F = Prep<E, DK, INV>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const int chunks = (p.T + C - 1) / C;
     const PrepArgs a{p.q, p.k, p.g, p.beta, p.lengths, records, p.B, p.Hk, p.H, p.T, chunks, p.bthd ? 1 : 0, p.scale};
@@ -116,20 +116,19 @@ cudaError_t launch(const Problem& p, uint8_t* records, cudaStream_t st) {
 }  // namespace
 
 size_t records_bytes(const Problem& p, bool gradients) {
-    const int rec = gradients ? record_bytes(2, 3) : record_bytes(1, p.bf16 ? 2 : 3);
-    return static_cast<size_t>(p.B) * p.H * ((p.T + C - 1) / C) * rec;
+    return static_cast<size_t>(p.B) * p.H * ((p.T + C - 1) / C) * record_bytes(gradients ? 2 : 1);
 }
 
-template <typename E, int PT, int INV>
+template <typename E, int INV>
 static cudaError_t by_width(const Problem& p, uint8_t* records, cudaStream_t st) {
-    if (p.d == 32) return launch<E, 32, PT, INV>(p, records, st);
-    if (p.d == 64) return launch<E, 64, PT, INV>(p, records, st);
-    return launch<E, 128, PT, INV>(p, records, st);
+    if (p.d == 32) return launch<E, 32, INV>(p, records, st);
+    if (p.d == 64) return launch<E, 64, INV>(p, records, st);
+    return launch<E, 128, INV>(p, records, st);
 }
 
 cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st) {
-    if (p.bf16) return gradients ? by_width<bf16, 3, 2>(p, records, st) : by_width<bf16, 2, 1>(p, records, st);
-    return gradients ? by_width<float, 3, 2>(p, records, st) : by_width<float, 3, 1>(p, records, st);
+    if (p.bf16) return gradients ? by_width<bf16, 2>(p, records, st) : by_width<bf16, 1>(p, records, st);
+    return gradients ? by_width<float, 2>(p, records, st) : by_width<float, 1>(p, records, st);
 }
 
 }  // namespace delta

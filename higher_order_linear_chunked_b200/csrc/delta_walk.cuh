@@ -60,9 +60,9 @@ struct Gates {
 };
 static_assert(sizeof(Gates) == 512, "a record's last piece");
 
-// Bytes of a chunk's record: `inverses` three-term inverses, P in PT terms, the gates.
+// Bytes of a chunk's record: `inverses` inverses and P, in three terms each, and the gates.
 constexpr int kXBytes = 3 * C * C * 2;
-constexpr int record_bytes(int inverses, int PT) { return inverses * kXBytes + PT * C * C * 2 + 512; }
+constexpr int record_bytes(int inverses) { return (inverses + 1) * kXBytes + 512; }
 
 __device__ __forceinline__ float ex2(float x) {      // 2^x to 2^-22, below 2^-126 zero
     float y;
@@ -196,8 +196,8 @@ __device__ __forceinline__ void finish_gates(Gates* s, float2* sum, float g, flo
 
 // 16 rows (16p..) of a chunk's decayed products with the keys, one warp.
 //   keys:  M = strict_low(D o K K^T) with a beta factor (rowbeta: beta_i, else beta_j), to mt[j][i]
-//   else:  P = scale low(D o Q K^T) as PT bf16 terms, to pt
-template <int DK, int KT, int PT>
+//   else:  P = scale low(D o Q K^T) as three bf16 terms, to pt
+template <int DK, int KT>
 __device__ __forceinline__ void products(bool keys, bool rowbeta, uint32_t kt, uint32_t at, const float2* sum, const float* beta,
                                          float* mt, uint8_t* pt, float scale, int p, int lane) {
     constexpr int RB = DK * 2, TERM = C * DK * 2;
@@ -247,10 +247,10 @@ __device__ __forceinline__ void products(bool keys, bool rowbeta, uint32_t kt, u
                 mt[j0 * kMS + i] = j0 < i ? x0 : 0.f;
                 mt[(j0 + 1) * kMS + i] = j0 + 1 < i ? x1 : 0.f;
             } else {
-                uint32_t t[PT];
-                split<PT>(j0 <= i ? x0 : 0.f, j0 + 1 <= i ? x1 : 0.f, t);
+                uint32_t t[3];
+                split<3>(j0 <= i ? x0 : 0.f, j0 + 1 <= i ? x1 : 0.f, t);
 #pragma unroll
-                for (int n = 0; n < PT; ++n)
+                for (int n = 0; n < 3; ++n)
                     *reinterpret_cast<uint32_t*>(pt + n * (C * C * 2) + piece<C * 2>(i, j0 >> 3) + (j0 & 7) * 2) = t[n];
             }
         }
