@@ -509,9 +509,6 @@ struct Blk {
     using Elem = E;
     static constexpr int DK = DK_, DV = DV_, N = N_, WARPS = N_ / 16, NT = 2 * WARPS * 32;
     static constexpr int KT = sizeof(E) == 2 ? 1 : 3;
-    // terms of what reaches only dq and dk (the pairs' products, which the sums for dg no longer see):
-    // to 2^-16 before a bf16 result's one rounding at 2^-9, in full for fp32
-    static constexpr int LT = KT == 1 ? 2 : 3;
     static constexpr int SW = 32;                       // value columns of a state at a time
     static constexpr int KTERM = N * DK * 2, OTERM = N * DV * 2, STERM = DK * SW * 2;
     static constexpr int k = 0, q = k + KT * KTERM, o = q + KT * KTERM, u = o + KT * OTERM, z = u + 3 * OTERM;
@@ -678,13 +675,10 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
             for (int t = 0; t < AT; ++t) ldsm4(x[t], at_rows_first<DV * 2>(sb + at + t * F::OTERM, r0, 2 * ks, lane));
 #pragma unroll
             for (int t = 0; t < YT; ++t) ldsm4(y[t], at_pieces_first<DV * 2>(sb + yt + t * F::OTERM, 16 * jb, 2 * ks, lane));
-            if constexpr (!ROWS && F::LT == 2) prod2<AT, YT>(w[0], w[1], x, y);
-            else prod2<AT, YT>(w[0], w[1], low[0], low[1], x, y);
+            prod2<AT, YT>(w[0], w[1], low[0], low[1], x, y);
         }
-        if constexpr (ROWS || F::LT == 3) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[0][j] += low[0][j], w[1][j] += low[1][j];
-        }
+        for (int j = 0; j < 4; ++j) w[0][j] += low[0][j], w[1][j] += low[1][j];
         const bool diagonal = jb == warp;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -732,23 +726,19 @@ __device__ __forceinline__ void with_pairs(float (&acc)[F::DK / 8][4], uint32_t 
                 }
             }
         }
-        uint32_t x[F::LT][4];
-        split_a<F::LT>(w[0], w[1], x);
+        uint32_t x[3][4];
+        split_a<3>(w[0], w[1], x);
 #pragma unroll
         for (int np = 0; np < DK / 16; ++np) {
             uint32_t y[KT][4];
 #pragma unroll
             for (int t = 0; t < KT; ++t) ldsm4t(y[t], at_rows_first<DK * 2>(sb + bt + t * F::KTERM, 16 * jb, 2 * np, lane));
-            if constexpr (F::LT == 2) {
-                prod2<2, KT>(acc[2 * np], acc[2 * np + 1], x, y);
-            } else {
-                float v[2][4] = {};
-                prod2<3, KT>(v[0], v[1], x, y);
+            float v[2][4] = {};
+            prod2<3, KT>(v[0], v[1], x, y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[2 * np][j] += v[0][j];
-                    acc[2 * np + 1][j] += v[1][j];
-                }
+            for (int j = 0; j < 4; ++j) {
+                acc[2 * np][j] += v[0][j];
+                acc[2 * np + 1][j] += v[1][j];
             }
         }
     }
@@ -954,7 +944,7 @@ __global__ void __launch_bounds__(F::NT, F::BLOCKS) k_delta_block_grads(const Bl
         by_row(acc, since, -1.f, r0, lane);
         row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, state_part);
         with_pairs<F, 3, 3, true, true>(acc, sb, sum, F::z, F::u, F::k, -1.f, lane, tile, F::k, pairs, cols + F::WARPS * N);
-        with_pairs<F, F::LT, F::LT, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, lane, tile);
+        with_pairs<F, 3, 3, false, true>(acc, sb, sum, F::u, F::z, F::k, -1.f, lane, tile);
 #pragma unroll
         for (int n = 0; n < DK / 8; ++n) pass[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
     } else {
@@ -965,7 +955,7 @@ __global__ void __launch_bounds__(F::NT, F::BLOCKS) k_delta_block_grads(const Bl
         float xs[2];
         by_row(acc, left, 1.f, r0, lane);
         row_dots<DK, KT>(acc, sm + F::k, F::KTERM, r0, lane, xs);
-        with_pairs<F, F::LT, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, lane, tile);
+        with_pairs<F, 3, KT, false, false>(acc, sb, sum, F::u, F::o, F::q, a.scale, lane, tile);
         if ((lane & 3) == 0) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) xj[r0 + (lane >> 2) + 8 * e] = xs[e];

@@ -92,3 +92,62 @@ def test_decayed_products_in_the_outputs(d):
     o = hla.gated_delta(*on(q, k, v, g, beta), scale=1.0)
     want, _ = od.forward(q, k, v, g, beta, 1.0)
     near(o[0, 0, 31], want[0, 0, 31], terms, "o")
+
+
+def test_pairs_in_dq():
+    """dq of the last token = the sum of w_j k_j, where w_j is what token j wrote: x and y in turn, on
+    keys with a small common part of alternating sign."""
+    d, T, n = 64, 32, 30
+    x = residues(n // 2, 7)
+    target = torch.stack([x, short(x)], 1).reshape(n).double()
+    k = torch.zeros(T, d)
+    k[:n, :n] = torch.eye(n)
+    k[:n, d - 1] = 2.0 ** -6 * torch.tensor([1.0, -1.0]).repeat(n // 2)
+    # beta_j such that token j writes its target, by the recurrence in 64 bits
+    beta, s = torch.zeros(T), torch.zeros(d, dtype=torch.float64)
+    for j in range(n):
+        beta[j] = float(target[j] / (1 - s @ k[j].double()))
+        s = s + float(beta[j]) * k[j].double() * (1 - s @ k[j].double())
+    v, dout = torch.zeros(1, 1, T, 32), torch.zeros(1, 1, T, 32)
+    v[0, 0, :n, 0], dout[0, 0, T - 1, 0] = 1.0, 1.0
+    q, k, v, dout = torch.zeros(1, 1, T, d).bfloat16(), k[None, None].bfloat16(), v.bfloat16(), dout.bfloat16()
+    g, beta = torch.zeros(1, 1, T), beta[None, None]
+    got = hla.gated_delta_backward(*on(q, k, v, g, beta, dout), scale=1.0)
+    want = od.backward(q, k, v, g, beta, 1.0, dout)["dq"][0, 0, T - 1]
+    assert float(want[d - 1]) > 2.0 ** -6 * 2.0 ** -18 * n / 2
+    near(got[0][0, 0, T - 1, d - 1], want[d - 1], 2.0 ** -6 * 1.5 * n, "dq")
+    near(got[0][0, 0, T - 1, :n], want[:n], 1.5, "dq")
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_pairs_in_dk(d):
+    """Token 0 writes (x, y) into two columns, and the gradients at the next output are 1 and -1 there."""
+    x = residues(1, 9)[0]
+    S = torch.zeros(1, 1, d, 32)
+    S[0, 0, 0, 0], S[0, 0, 0, 1] = -x, -short(x)
+    q, k, v, dout = (torch.zeros(1, 1, 2, w) for w in (d, d, 32, 32))
+    k[0, 0, 0, 0] = q[0, 0, 1, 1] = dout[0, 0, 1, 0] = 1.0
+    dout[0, 0, 1, 1] = -1.0
+    q, k, v, dout = (t.bfloat16() for t in (q, k, v, dout))
+    g, beta = torch.zeros(1, 1, 2), torch.ones(1, 1, 2)
+    got = hla.gated_delta_backward(*on(q, k, v, g, beta, dout), scale=1.0, initial_state=S.to(DEV))
+    want = od.backward(q, k, v, g, beta, 1.0, dout, S)["dk"][0, 0, 0]
+    assert float(want[1]) > 2.0 ** -18
+    near(got[1][0, 0, 0], want, 2 * 1.5, "dk")
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_shared_heads_in_dk(d):
+    """The same over two value heads of one key head: x of the first, -y of the second."""
+    x = residues(1, 9)[0]
+    S = torch.zeros(1, 2, d, 32)
+    S[0, 0, 0, 0], S[0, 1, 0, 0] = -x, -short(x)
+    q, k, v, dout = (torch.zeros(1, h, 2, w) for h, w in ((1, d), (1, d), (2, 32), (2, 32)))
+    k[0, 0, 0, 0] = q[0, 0, 1, 1] = dout[0, 0, 1, 0] = 1.0
+    dout[0, 1, 1, 0] = -1.0
+    q, k, v, dout = (t.bfloat16() for t in (q, k, v, dout))
+    g, beta = torch.zeros(1, 2, 2), torch.ones(1, 2, 2)
+    got = hla.gated_delta_backward(*on(q, k, v, g, beta, dout), scale=1.0, initial_state=S.to(DEV))
+    want = od.backward(q, k, v, g, beta, 1.0, dout, S)["dk"][0, 0, 0]
+    assert float(want[1]) > 2.0 ** -18
+    near(got[1][0, 0, 0], want, 2 * 1.5, "dk")
