@@ -159,11 +159,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
 #pragma unroll
                     for (int j = 0; j < 4; ++j) z[n][j] = fmaf((j & 1) ? f.y : f.x, y[n][j], z[n][j]);
                 }
-                const float all = G->all;
-#pragma unroll
-                for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[n][j] *= all;
                 // H^T = dU^T X'; X'[j][i] is zero for j < i
                 float r[4][4] = {};
 #pragma unroll
@@ -190,22 +185,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
                     }
                 }
                 // dS0^T: the outputs' share from the side warp, and -(e^c K)^T Z, transposed
-                {
-                    const float4* sd = reinterpret_cast<const float4*>(sm + F::side + (c & 1) * F::SIDE) + grp * (DK / 8) * 32 + lane;
-#pragma unroll
-                    for (int n = 0; n < DK / 8; ++n) {
-                        const float4 x = sd[n * 32];
-                        S[n][0] += x.x; S[n][1] += x.y; S[n][2] += x.z; S[n][3] += x.w;
-                    }
-                }
+                uint32_t au[2][3][4];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t au[3][4], bt[DK / 16][KT][4];
-#pragma unroll
-                    for (int np = 0; np < DK / 16; ++np)
-#pragma unroll
-                        for (int t = 0; t < KT; ++t)
-                            ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 f = *reinterpret_cast<const float2*>(&G->since[16 * kk + 8 * e + 2 * (lane & 3)]);
@@ -213,8 +195,28 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
 #pragma unroll
                         for (int j = 0; j < 4; ++j) r[2 * kk + e][j] *= (j & 1) ? -f.y * be.y : -f.x * be.x;
                     }
-                    split_a<3>(r[2 * kk], r[2 * kk + 1], au);
-                    prod<3, KT, DK / 16>(S, au, bt);
+                    split_a<3>(r[2 * kk], r[2 * kk + 1], au[kk]);
+                }
+                const float4* sd = reinterpret_cast<const float4*>(sm + F::side + (c & 1) * F::SIDE) + grp * (DK / 8) * 32 + lane;
+#pragma unroll
+                for (int g = 0; g < DK / 32; ++g) {
+                    float W[4][4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float4 x = sd[(4 * g + n) * 32];
+                        W[n][0] = x.x; W[n][1] = x.y; W[n][2] = x.z; W[n][3] = x.w;
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        uint32_t bt[2][KT][4];
+#pragma unroll
+                        for (int np = 0; np < 2; ++np)
+#pragma unroll
+                            for (int t = 0; t < KT; ++t)
+                                ldsm4t(bt[np][t], ((k_t + so) ^ ((2 * g + np) << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                        prod<3, KT, 2>(W, au[kk], bt);
+                    }
+                    decay_and_add(S + 4 * g, G->all, W);
                 }
             } else {
             // this part's share of dS^T K^T, all tokens
@@ -315,11 +317,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
                 for (int t = 0; t < 3; ++t)
                     reinterpret_cast<uint2*>(yf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
             }
-            const float all = G->all;
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) S[n][j] *= all;
+            float W[DH / 8][4] = {};
             ptx::named_sync(1 + grp, NH * 32);
             // scale (e^c Q)^T dO, transposed: all parts have shared theirs by now
 #pragma unroll
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
 #pragma unroll
                     for (int t = 0; t < KT; ++t)
                         ldsm4t(bq[np][t], ((q_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
-                prod<3, KT, DH / 16>(S, au, bq);
+                prod<3, KT, DH / 16>(W, au, bq);
             }
             // H^T = dU^T X' for the tokens of this part; X'[j][i] is zero above the diagonal (j < i)
             uint32_t ay[2][3][4];
@@ -387,8 +385,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
 #pragma unroll
                     for (int t = 0; t < KT; ++t)
                         ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
-                prod<3, KT, DH / 16>(S, au, bt);
+                prod<3, KT, DH / 16>(W, au, bt);
             }
+            decay_and_add(S, G->all, W);
             }
             if (++stage == F::NS) stage = 0;
             step_end();

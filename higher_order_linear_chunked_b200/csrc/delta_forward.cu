@@ -79,7 +79,9 @@ struct Cfg {
     static constexpr int yf = ex + (NH > 1 ? W_STATE * 2048 : 0);    // Y of the chunk as an A operand; the decayed U
     static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
     static constexpr int bytes = yf + (NH > 1 ? NG_ * YB : 0);
-    static constexpr int BLOCKS = bytes <= 113 * 1024 ? 2 : 1;   // of an SM
+    // of an SM; summaries of narrow bf16 heads are four warps and 38 kB, so that 128 registers a thread let
+    // four share one (1x4x16384x64: 110 us, with three 126)
+    static constexpr int BLOCKS = MODE_ == SUMMARY && BF && DK_ <= 64 ? 4 : bytes <= 113 * 1024 ? 2 : 1;
 };
 
 template <typename F>
@@ -217,19 +219,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     }
                 }
                 // U^T for the outputs, and U^T e^(c_C - c) for the state
-                const float all = G->all;
-#pragma unroll
-                for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[n][j] *= all;
+                uint32_t au[2][3][4];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t au[3][4], bt[DK / 16][KT][4];
-#pragma unroll
-                    for (int np = 0; np < DK / 16; ++np)
-#pragma unroll
-                        for (int t = 0; t < KT; ++t)
-                            ldsm4t(bt[np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
 #pragma unroll
                     for (int n = 2 * kk; n < 2 * kk + 2; ++n) {
                         const float2 be = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
@@ -249,8 +241,23 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 #pragma unroll
                         for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? f.y : f.x;
                     }
-                    split_a<3>(r[2 * kk], r[2 * kk + 1], au);
-                    prod<3, KT, DK / 16>(S, au, bt);
+                    split_a<3>(r[2 * kk], r[2 * kk + 1], au[kk]);
+                }
+                // 32 keys at a time: four tiles cover a product's latency
+#pragma unroll
+                for (int g = 0; g < DK / 32; ++g) {
+                    float W[4][4] = {};
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        uint32_t bt[2][KT][4];
+#pragma unroll
+                        for (int np = 0; np < 2; ++np)
+#pragma unroll
+                            for (int t = 0; t < KT; ++t)
+                                ldsm4t(bt[np][t], ((k_t + so) ^ ((2 * g + np) << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
+                        prod<3, KT, 2>(W, au[kk], bt);
+                    }
+                    decay_and_add(S + 4 * g, G->all, W);
                 }
             } else {
             // this part's share of S0^T K^T, all tokens
@@ -320,10 +327,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 for (int t = 0; t < 3; ++t)
                     reinterpret_cast<uint2*>(yf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
             }
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) S[n][j] *= all;
             ptx::named_sync(1 + grp, NH * 32);
             // R^T = Y^T X^T for the tokens of this part; X is lower triangular
             uint32_t ay[2][3][4];
@@ -381,6 +384,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                         ldsm4t(bt[kk][np][0], ((k_t + so) ^ (np << 5)) + kk * 16 * DK * 2);
             }
             ptx::named_sync(1 + grp, NH * 32);
+            float W[DH / 8][4] = {};
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 uint32_t au[3][4];
@@ -396,8 +400,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                         for (int t = 0; t < KT; ++t)
                             ldsm4t(bt[kk][np][t], ((k_t + so) ^ (np << 5)) + t * (C * DK * 2) + kk * 16 * DK * 2);
                 }
-                prod<3, KT, DH / 16>(S, au, bt[kk]);
+                prod<3, KT, DH / 16>(W, au, bt[kk]);
             }
+            decay_and_add(S, all, W);
             }
             if (++stage == F::NS) stage = 0;
             if (++gstage == F::NG_STAGES) gstage = 0;

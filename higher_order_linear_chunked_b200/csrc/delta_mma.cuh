@@ -94,6 +94,17 @@ __device__ __forceinline__ void prod2(float (&h0)[4], float (&h1)[4], float (&l0
     mma16816(h1, a[0], b[0][2], b[0][3]);
 }
 
+// S = f S + W, rounded once: a carried state is not itself an accumulator of the products, which would
+// cut it at its last bit once a product, always towards zero, so that a state that forgets slowly lost
+// 1e-4 of itself in 512 chunks.
+template <int NT>
+__device__ __forceinline__ void decay_and_add(float (*S)[4], float f, const float (&W)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[n][j] = fmaf(S[n][j], f, W[n][j]);
+}
+
 // The bf16 terms of a pair, packed (x0 in the low half).
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&t)[N]) {
