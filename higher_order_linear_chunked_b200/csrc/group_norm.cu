@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads) k_group_norm(const Args a, int lg, b
 
 // A group of lanes keeps one group column and walks the rows slot, slot + slots, ..., the next row on
 // its way while it works on one; its sums over those rows go to row `slot` of the partial sums.  Lanes
-// and rows past the end hold zeros, which add nothing.
+// and rows past the end hold zeros, which add nothing: such rows are normalised with eps = 1, since with
+// an eps of 0 their zeros would become 0 / 0.
 template <typename E, int VEC, int IT, int FLAGS>
 __global__ void __launch_bounds__(kThreads, IT == 1 ? 3 : 1) k_group_norm_grad(const Args a, int lg, int slots, bool wide) {
     const Form<FLAGS> form(a);
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, IT == 1 ? 3 : 1) k_group_norm_grad(c
             if (form.gate) rt[i].get(t[i]);
         }
         ask(row + slots, at + step);
-        const float r = normalise<VEC, IT>(x, on, L, a.inv, a.eps, form.center);
+        const float r = normalise<VEC, IT>(x, on, L, a.inv, live ? a.eps : 1.f, form.center);
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {

@@ -1,0 +1,37 @@
+"""Group norm on the GPU where eps or the activation's argument is at its edge (oracle/delta.py in 64 bits)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import higher_order_linear_chunked_b200 as hla  # noqa: E402
+from higher_order_linear_chunked_b200 import delta  # noqa: E402
+from oracle import delta as od  # noqa: E402
+from test_gpu_group_norm import DEV, DT, check, inputs  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("activation", ["none", "silu"])
+@pytest.mark.parametrize("center", [True, False])
+def test_no_eps(dtype, gated, activation, center):
+    """eps = 0 over more rows than the gradient kernel walks at once, and not a multiple of them.
+    Tolerances as in test_gpu_group_norm.py: the sums' terms are |dz n| and |dz|."""
+    rows, groups, width = 1000, 64, 32
+    x, dy, gate, w, b = inputs(dtype, rows, groups, width, gated, True, 17)
+    C = groups * width
+    slots = delta._library().hla_group_norm_backward_workspace_bytes(hla.HLA_BF16 if dtype == "bf16" else hla.HLA_F32, rows,
+                                                                     C, groups) // (8 * C)
+    assert rows > slots and rows % slots
+    how = dict(eps=0.0, activation=activation, center=center)
+    dev = [t.to(DEV) if t is not None else None for t in (x, dy, w, b, gate)]
+    got = hla.group_norm_backward(dev[0], dev[1], groups, *dev[2:], **how)
+    want = od.group_norm_backward(x, dy, groups, w, b, gate, **how)
+    size = dy.double().abs() * (gate.double().abs().clamp(min=1.0) if gated else 2.0)
+    n = od.group_norm(x, groups, eps=0.0, center=center).abs()
+    check(got[2], want[2], 2.4e-5 * (size * n).sum(0), "dweight")
+    check(got[3], want[3], 2.4e-5 * size.sum(0), "dbias")
+    xg = x.double().reshape(rows, groups, width)
+    xg = xg - xg.mean(-1, keepdim=True) if center else xg
+    r = 1 / torch.sqrt((xg * xg).mean(-1, keepdim=True))
+    check(got[0], want[0], 2e-5 * float((r * (size * w.double().abs()).reshape(xg.shape)).max()), "dx")
