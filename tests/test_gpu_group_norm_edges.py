@@ -35,3 +35,17 @@ def test_no_eps(dtype, gated, activation, center):
     xg = xg - xg.mean(-1, keepdim=True) if center else xg
     r = 1 / torch.sqrt((xg * xg).mean(-1, keepdim=True))
     check(got[0], want[0], 2e-5 * float((r * (size * w.double().abs()).reshape(xg.shape)).max()), "dx")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activation_in_a_weight_gradient(dtype):
+    """One row of pairs (1, -1): n is 1 and -1, so that dweight, fp32 for either type, is +-silu(gate).
+    Relative room: rsqrt and exp 2^-22 each, six roundings of 2^-24."""
+    gate = torch.linspace(-80, 20, 4096).to(DT[dtype])[None]
+    x = torch.tensor([1.0, -1.0]).repeat(2048).to(DT[dtype])[None]
+    w = torch.ones(4096)
+    how = dict(eps=0.0, activation="silu", center=False)
+    dw = hla.group_norm_backward(x.to(DEV), torch.ones_like(x).to(DEV), 2048, weight=w.to(DEV), gate=gate.to(DEV), **how)[2]
+    want = od.group_norm_backward(x, torch.ones_like(x), 2048, w, None, gate, **how)[2]
+    off = ((dw.cpu().double() - want).abs() / want.abs().clamp(min=1e-300))[gate[0] != 0]
+    assert float(off.max()) <= 14 * 2.0 ** -24
