@@ -19,6 +19,7 @@ struct Problem {
     bool bf16;
     bool bthd;
     float scale;
+    int* status;             // the workspace's status word, which prepare() clears; null without a workspace
 };
 
 // Chunk by chunk on the tensor cores (delta_forward.cu), with forward_bytes() of workspace.
@@ -26,7 +27,8 @@ size_t forward_bytes(const Problem& p);
 int forward_launches(const Problem& p);
 cudaError_t forward(const Problem& p, void* ws, cudaStream_t st);
 
-// The chunks' records (delta_prepare.cu); gradients: the form that the backward pass reads.
+// The chunks' records (delta_prepare.cu); gradients: the form that the backward pass reads.  The first
+// kernel of every call with a workspace: it clears the status word.
 size_t records_bytes(const Problem& p, bool gradients);
 cudaError_t prepare(const Problem& p, bool gradients, uint8_t* records, cudaStream_t st);
 

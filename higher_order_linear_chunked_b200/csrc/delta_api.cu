@@ -76,7 +76,7 @@ hla_status_t hla_delta_forward(const void* q, const void* k, const void* v, cons
     if (misaligned(workspace, 16)) return HLA_ERR_ALIGN;
     if (workspace_bytes < forward_workspace(dtype, B, Hk, H, T, d, dv)) return HLA_ERR_WORKSPACE;
     const hla::delta::Problem p{q, k, v, g, beta, state_in, lengths, o, state_out, B, Hk, H, T, d, dv,
-                                dtype == HLA_BF16, layout == HLA_BTHD, scale};
+                                dtype == HLA_BF16, layout == HLA_BTHD, scale, static_cast<int*>(workspace)};
     void* body = static_cast<char*>(workspace) + hla::kStatusBytes;
     return hla::delta::forward(p, body, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
@@ -91,7 +91,7 @@ hla_status_t hla_delta_step(float* state, const void* q, const void* k, const vo
         misaligned(g, 4) || misaligned(beta, 4))
         return HLA_ERR_ALIGN;
     const hla::delta::Problem p{q, k, v, g, beta, state, nullptr, o, state, B, Hk, H, 1, d, dv,
-                                dtype == HLA_BF16, false, scale};
+                                dtype == HLA_BF16, false, scale, nullptr};
     return hla::delta::recur(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
 
@@ -127,6 +127,7 @@ hla_status_t hla_delta_backward(const void* q, const void* k, const void* v, con
     p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.state_in = state_in; p.lengths = lengths;
     p.bthd = layout == HLA_BTHD;
     p.scale = scale;
+    p.status = static_cast<int*>(workspace);
     const hla::delta::Gradients gr{dout, dstate_out, dq, dk, dv_out, dg, dbeta, dstate_in};
     void* body = static_cast<char*>(workspace) + hla::kStatusBytes;
     return hla::delta::backward(p, gr, body, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;

@@ -18,6 +18,7 @@ struct PrepArgs {
     const float *g, *beta;
     const int* lengths;
     uint8_t* records;          // [B*H][chunks][record]
+    int* status;
     int B, Hk, H, T, chunks, bthd;
     float scale;
 };
@@ -57,6 +58,7 @@ __global__ void __launch_bounds__(F::WARPS * 32) k_delta_prepare(const PrepArgs 
     const int bh = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
     const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
     const int rows = min(C, length_of(a.lengths, b, a.T) - c * C);
+    if (blockIdx.x == 0 && tid == 0) *a.status = DEV_OK;               // no kernel of these calls sets it
     if (rows <= 0) return;                                              // no walk reads this chunk
     const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.H);
     const long long kr = row_of(a.bthd, b, hk, a.Hk, c * C, a.T), vr = row_of(a.bthd, b, h, a.H, c * C, a.T);
@@ -106,7 +108,7 @@ cudaError_t launch(const Problem& p, uint8_t* records, cudaStream_t st) {
     using F = Prep<E, DK, INV>;
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const int chunks = (p.T + C - 1) / C;
-    const PrepArgs a{p.q, p.k, p.g, p.beta, p.lengths, records, p.B, p.Hk, p.H, p.T, chunks, p.bthd ? 1 : 0, p.scale};
+    const PrepArgs a{p.q, p.k, p.g, p.beta, p.lengths, records, p.status, p.B, p.Hk, p.H, p.T, chunks, p.bthd ? 1 : 0, p.scale};
     const cudaError_t e = allow_smem<k_delta_prepare<F>>(F::bytes);
     if (e != cudaSuccess) return e;
     k_delta_prepare<F><<<p.B * p.H * chunks, F::WARPS * 32, F::bytes, st>>>(a);

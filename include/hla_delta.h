@@ -2,7 +2,8 @@
  * hla_delta.h - C ABI of the gated delta rule and of the group norm that stands around it.
  *
  * Part of libhla.so; status codes, element types, streams, memory ownership and error
- * behaviour are those of hla.h.
+ * behaviour are those of hla.h.  The rule's workspaces begin with a device status word as those do (a
+ * call clears it, and none of these kernels has a wait that could run out); the norm's holds sums only.
  *
  * Gated delta rule.  Every value head keeps a matrix S [d][dv] (fp32).  Token t with query q_t,
  * key k_t, value v_t, log decay g_t and write strength beta_t does
