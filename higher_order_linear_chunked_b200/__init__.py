@@ -150,6 +150,16 @@ def _check(q, k, v):
         raise ValueError("shape mismatch: q, k [B,H,T,d], v [B,H,T,dv]")
 
 
+def _check_workspace(workspace, device):
+    """A caller's workspace: its bytes lie in one piece on the call's device (the C boundary sees a size only)."""
+    if not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor (this library has no CPU path)")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the call's tensors on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def workspace_bytes(op: int, dtype_code: int, decayed: bool, B: int, H: int, T: int, d: int, dv: int) -> int:
     return int(load_library().hla_workspace_bytes(op, dtype_code, int(bool(decayed)), B, H, T, d, dv))
 

@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import HLAError, HLA_BF16, HLA_F32, HLA_OK, load_library as _load
+from . import HLAError, HLA_BF16, HLA_F32, HLA_OK, _check_workspace, load_library as _load
 
 LAYOUTS = {"bhtd": 0, "bthd": 1}
 ACTIVATIONS = ("none", "silu")
@@ -198,6 +198,8 @@ def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=N
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         _keep(on, stream, workspace)
+    else:
+        _check_workspace(workspace, dev)
     _call(on, lib.hla_delta_forward, "hla_delta_forward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), out.data_ptr(), _ptr(state_out), B, Hk,
             H, T, d, dv, code, LAYOUTS[layout], d ** -0.5 if scale is None else scale, workspace.data_ptr(),
@@ -252,6 +254,8 @@ def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, 
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        _check_workspace(workspace, dev)
     dq, dk, dvv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
     dstate0 = torch.empty_like(initial_state) if initial_state is not None else None
     _keep(on, stream, dq, dk, dvv, dg, dbeta, dstate0, workspace)
@@ -326,6 +330,8 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
     dweight = torch.empty_like(weight) if weight is not None else None
     dbias = torch.empty_like(bias) if bias is not None else None
     nbytes = 0
+    if workspace is not None:
+        _check_workspace(workspace, x.device)
     if weight is not None or bias is not None:
         if workspace is None:
             n = _bytes("hla_group_norm_backward_workspace_bytes", _CODES[x.dtype], rows, C, groups)
