@@ -203,6 +203,8 @@ def _call(op: int, q, k, v, gamma=None, eps: float = 1e-6, out=None, workspace=N
             raise ValueError("gamma must be a contiguous CUDA float32 tensor of shape [H]")
     if workspace is None:
         workspace = make_workspace(op, q, v, decayed=gamma is not None)
+    else:
+        _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
     sptr = ctypes.c_void_p(st.cuda_stream)
     gptr = ctypes.c_void_p(gamma.data_ptr()) if gamma is not None else ctypes.c_void_p(0)
@@ -280,6 +282,8 @@ def _backward(op, q, k, v, dout, workspace, stream, eps):
         raise HLAError(5, "no backward kernel for this shape/dtype")
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace, q.device)
     dq = torch.empty((B, H, T, d), dtype=torch.float32, device=q.device)
     dk = torch.empty_like(dq)
     dv = torch.empty((B, H, T, dvd), dtype=torch.float32, device=q.device)
@@ -358,6 +362,8 @@ def forward_profiled(op_name: str, q, k, v, events, gamma=None, eps: float = 1e-
     op = OP_CODES[op_name]
     if workspace is None:
         workspace = make_workspace(op, q, v, decayed=gamma is not None)
+    else:
+        _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
     handles = (ctypes.c_void_p * 4)(*[ctypes.c_void_p(e.cuda_event) for e in events])
     rc = lib.hla_forward_profiled(
@@ -427,6 +433,8 @@ def state(op_name: str, q, k, v, gamma=None, out=None, workspace=None, stream=No
         if nb == 0:
             raise HLAError(5, "unsupported shape/dtype for this op")
         workspace = torch.empty(nb, dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
     rc = lib.hla_state(op, ctypes.c_void_p(q.data_ptr()), ctypes.c_void_p(k.data_ptr()),
                        ctypes.c_void_p(v.data_ptr()), ctypes.c_void_p(out.data_ptr()), B, H, T, d, dv,
