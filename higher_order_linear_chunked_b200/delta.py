@@ -7,7 +7,9 @@
   normalised, with an activation or a gate.
 
 As in the package's other calls the library's kernels do all the work, on the tensors' device and
-the current torch stream; arguments are checked here and again at the C boundary.
+the current torch stream; arguments are checked here and again at the C boundary.  A call on another
+stream (``stream=``) takes what it allocates from that stream's memory; ordering that stream behind the
+inputs, and the use of the results behind it, is the caller's.
 """
 from __future__ import annotations
 
@@ -76,12 +78,24 @@ def _stream_of(device: int, stream) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _keep(device: int, stream, *tensors) -> None:
-    """What a call allocated on the current stream is kept for the stream that uses it."""
-    if stream is not None and stream.cuda_stream != _raw_stream(device):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _new(on: int, stream, result: bool, make, *args, **kw):
+    """What a call allocates, from the memory of the stream that writes it: a block of the current stream's
+    memory may still be in use by work queued there.  A result is kept for the current stream too."""
+    if stream is None:
+        return make(*args, **kw)
+    current = torch.cuda.current_stream(on)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if result and stream != current:
+        t.record_stream(current)
+    return t
+
+
+def _given(workspace, device, stream):
+    """A caller's workspace, checked, and kept for the stream that uses it."""
+    _check_workspace(workspace, device)
+    if stream is not None:
+        workspace.record_stream(stream)
 
 
 def _call(device: int, fn, what, *args) -> None:
@@ -182,24 +196,21 @@ def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=N
     on = q.get_device()
     lib = _library()
     if out is None:
-        out = torch.empty_like(v)
-        _keep(on, stream, out)
+        out = _new(on, stream, True, torch.empty_like, v)
     else:
         _expect("out", out, tuple(v.shape), v.dtype, dev)
     if state_out is not None:
         _expect("state_out", state_out, (B, H, d, dv), torch.float32, dev)
     elif return_state:
-        state_out = torch.empty((B, H, d, dv), dtype=torch.float32, device=dev)
-        _keep(on, stream, state_out)
+        state_out = _new(on, stream, True, torch.empty, (B, H, d, dv), dtype=torch.float32, device=dev)
     code = _CODES[q.dtype]
     if workspace is None:
         n = _bytes("hla_delta_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        _keep(on, stream, workspace)
+        workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=dev)
     else:
-        _check_workspace(workspace, dev)
+        _given(workspace, dev, stream)
     _call(on, lib.hla_delta_forward, "hla_delta_forward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), out.data_ptr(), _ptr(state_out), B, Hk,
             H, T, d, dv, code, LAYOUTS[layout], d ** -0.5 if scale is None else scale, workspace.data_ptr(),
@@ -216,9 +227,7 @@ def gated_delta_step(state, q, k, v, g, beta, scale: Optional[float] = None, out
             state.is_contiguous()):
         _expect("state", state, (B, H, d, dv), torch.float32, q.device)
     if out is None:
-        out = torch.empty_like(v)
-        if stream is not None:
-            _keep(on, stream, out)
+        out = _new(on, stream, True, torch.empty_like, v)
     else:
         _expect("out", out, tuple(v.shape), v.dtype, q.device)
     _call(on, _library().hla_delta_step, "hla_delta_step rejected the call", state.data_ptr(), q.data_ptr(),
@@ -253,12 +262,11 @@ def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, 
         n = _bytes("hla_delta_backward_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=dev)
     else:
-        _check_workspace(workspace, dev)
-    dq, dk, dvv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
-    dstate0 = torch.empty_like(initial_state) if initial_state is not None else None
-    _keep(on, stream, dq, dk, dvv, dg, dbeta, dstate0, workspace)
+        _given(workspace, dev, stream)
+    dq, dk, dvv, dg, dbeta = (_new(on, stream, True, torch.empty_like, t) for t in (q, k, v, g, beta))
+    dstate0 = _new(on, stream, True, torch.empty_like, initial_state) if initial_state is not None else None
     _call(on, lib.hla_delta_backward, "hla_delta_backward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), dout.data_ptr(), _ptr(dstate),
             dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dstate0), B, Hk, H, T, d,
@@ -306,9 +314,7 @@ def group_norm(x, groups: int, weight=None, bias=None, gate=None, eps: float = 1
     C, rows, flags = _norm_args(x, groups, weight, bias, gate, activation, center)
     on = x.get_device()
     if out is None:
-        out = torch.empty_like(x)
-        if stream is not None:
-            _keep(on, stream, out)
+        out = _new(on, stream, True, torch.empty_like, x)
     else:
         _expect("out", out, tuple(x.shape), x.dtype, x.device)
     _call(on, _library().hla_group_norm_forward, "hla_group_norm_forward rejected the call", x.data_ptr(), _ptr(gate),
@@ -325,21 +331,18 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
     _expect("dy", dy, tuple(x.shape), x.dtype, x.device)
     on = x.get_device()
     lib = _library()
-    dx = torch.empty_like(x)
-    dgate = torch.empty_like(gate) if gate is not None else None
-    dweight = torch.empty_like(weight) if weight is not None else None
-    dbias = torch.empty_like(bias) if bias is not None else None
+    dx, dgate, dweight, dbias = (_new(on, stream, True, torch.empty_like, t) if t is not None else None
+                                 for t in (x, gate, weight, bias))
     nbytes = 0
     if workspace is not None:
-        _check_workspace(workspace, x.device)
+        _given(workspace, x.device, stream)
     if weight is not None or bias is not None:
         if workspace is None:
             n = _bytes("hla_group_norm_backward_workspace_bytes", _CODES[x.dtype], rows, C, groups)
             if n == 0:
                 raise HLAError(5, f"no group norm kernel for {rows} rows of {C} channels in {groups} groups")
-            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+            workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=x.device)
         nbytes = workspace.numel() * workspace.element_size()
-    _keep(on, stream, dx, dgate, dweight, dbias, workspace)
     _call(on, lib.hla_group_norm_backward, "hla_group_norm_backward rejected the call", x.data_ptr(), _ptr(gate),
             _ptr(weight), _ptr(bias), dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dweight), _ptr(dbias), rows, C,
             groups, _CODES[x.dtype], eps, flags, _ptr(workspace), nbytes, _stream_of(on, stream))
