@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int kDeltaAbiVersion = 1;
+constexpr int kMaxTokens = 0x7fffffff - 63;   // rounded up to blocks of 64 still an int
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
@@ -19,7 +20,7 @@ hla_status_t check_shape(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, 
     if (dtype != HLA_F32 && dtype != HLA_BF16) return HLA_ERR_DTYPE;
     if (B < 1 || Hk < 1 || H < 1 || T < 1 || d < 1 || dv < 1) return HLA_ERR_SHAPE;
     if ((long long)B * H > (1LL << 24) || (long long)B * H * T >= (1LL << 31)) return HLA_ERR_SHAPE;
-    if (H % Hk != 0) return HLA_ERR_SHAPE;
+    if (T > kMaxTokens || H % Hk != 0) return HLA_ERR_SHAPE;
     if (!width_ok(d) || !width_ok(dv)) return HLA_ERR_UNSUPPORTED;
     return HLA_OK;
 }

@@ -18,7 +18,7 @@
  * uses query/key head h / (H / Hk).  States are [B][H][d][dv].  Base addresses are 16-byte
  * aligned (g, beta, lengths: 4-byte).
  *
- * Supported shapes.  d and dv each in {32, 64, 128}; T >= 1; B, Hk, H >= 1; B*H <= 2^24,
+ * Supported shapes.  d and dv each in {32, 64, 128}; 1 <= T <= 2^31 - 64; B, Hk, H >= 1; B*H <= 2^24,
  * B*H*T < 2^31.  Anything else returns HLA_ERR_UNSUPPORTED or HLA_ERR_SHAPE before any launch.
  * Outputs must not overlap inputs or one another, except where a call says so.
  *
