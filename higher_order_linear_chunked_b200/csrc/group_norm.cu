@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, IT == 1 ? 3 : 1) k_group_norm_grad(c
     }
     if (!a.partial || !mine) return;
     float* pw = a.partial + slot * 2 * a.C + wbase;
+    float* pb = pw + a.C;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int e = (i * L + in) * VEC;
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, IT == 1 ? 3 : 1) k_group_norm_grad(c
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             pw[e + j] = dw[i][j];
-            pw[a.C + e + j] = db[i][j];
+            pb[e + j] = db[i][j];
         }
     }
 }
@@ -314,9 +315,9 @@ __global__ void __launch_bounds__(1024) k_group_norm_columns(const float* partia
                                                              float* dbias) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    const long long both = 2LL * C, c = static_cast<long long>(blockIdx.x) * 32 + lane;   // over an int from 2^30 channels on
     float sum = 0.f;
-    if (c < 2 * C) {
+    if (c < both) {
 #pragma unroll 8
         for (int r = part; r < slots; r += 32) sum += partial[static_cast<long long>(r) * 2 * C + c];
     }
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(1024) k_group_norm_columns(const float* partia
     __syncthreads();
     sum = s[lane][part];                     // column `part` of the block, its 32 sums over the lanes
     sum = lanes_sum(sum, 32);
-    const int col = blockIdx.x * 32 + part;
+    const long long col = static_cast<long long>(blockIdx.x) * 32 + part;
     float* out = col < C ? dweight : dbias;
-    if (lane == 0 && col < 2 * C && out) out[col < C ? col : col - C] = sum;
+    if (lane == 0 && col < both && out) out[col < C ? col : col - C] = sum;
 }
 
 struct Shape { int vec, it, lg; };
@@ -434,7 +435,7 @@ cudaError_t backward(const Args& given, bool is_bf16, cudaStream_t st) {
     pick(is_bf16, s, flags_of(a), Backward{a, s.lg, slots, st});
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
-    k_group_norm_columns<<<(2 * a.C + 31) / 32, 1024, 0, st>>>(a.partial, slots, a.C, a.dweight, a.dbias);
+    k_group_norm_columns<<<static_cast<unsigned>((2LL * a.C + 31) / 32), 1024, 0, st>>>(a.partial, slots, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }
 

@@ -49,3 +49,22 @@ def test_activation_in_a_weight_gradient(dtype):
     want = od.group_norm_backward(x, torch.ones_like(x), 2048, w, None, gate, **how)[2]
     off = ((dw.cpu().double() - want).abs() / want.abs().clamp(min=1e-300))[gate[0] != 0]
     assert float(off.max()) <= 14 * 2.0 ** -24
+
+
+def test_many_channels():
+    """2^30 channels, whose two column sums together are more than an int counts: without weight, gate and
+    activation the gradient of the bias is dy, and each group's dx sums to nothing."""
+    C = 1 << 30
+    x = torch.ones(1, C, dtype=torch.bfloat16, device=DEV)
+    x[0, ::2] = -1.0
+    dy = torch.ones_like(x)
+    dy[0, ::3] = 2.0
+    dx, _, dw, db = hla.group_norm_backward(x, dy, C // 64, bias=torch.zeros(C, device=DEV))
+    assert dw is None
+    for lo in range(0, C, 1 << 27):
+        hi = lo + (1 << 27)
+        assert torch.equal(db[lo:hi], dy[0, lo:hi].float())
+    last = od.group_norm_backward(x[:, -64:].cpu(), dy[:, -64:].cpu(), 1)[0]
+    check(dx[:, -64:], last, 1e-5, "dx")
+    del x, dy, dx, db
+    torch.cuda.empty_cache()
