@@ -78,17 +78,28 @@ def _stream_of(device: int, stream) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _new(on: int, stream, result: bool, make, *args, **kw):
-    """What a call allocates, from the memory of the stream that writes it: a block of the current stream's
-    memory may still be in use by work queued there.  A result is kept for the current stream too."""
+def _empty(stream, size, dtype, device):
+    """What a call works in, from the memory of the stream that uses it: a block of the current stream's
+    memory may still be in use by work queued there."""
     if stream is None:
-        return make(*args, **kw)
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
+def _likes(on: int, stream, *tensors):
+    """Results shaped like the given tensors (None for None), allocated in the same way and kept for the
+    current stream too."""
+    if stream is None:
+        return [torch.empty_like(t) if t is not None else None for t in tensors]
     current = torch.cuda.current_stream(on)
     with torch.cuda.stream(stream):
-        t = make(*args, **kw)
-    if result and stream != current:
-        t.record_stream(current)
-    return t
+        made = [torch.empty_like(t) if t is not None else None for t in tensors]
+    if stream != current:
+        for t in made:
+            if t is not None:
+                t.record_stream(current)
+    return made
 
 
 def _given(workspace, device, stream):
@@ -196,19 +207,21 @@ def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=N
     on = q.get_device()
     lib = _library()
     if out is None:
-        out = _new(on, stream, True, torch.empty_like, v)
+        out, = _likes(on, stream, v)
     else:
         _expect("out", out, tuple(v.shape), v.dtype, dev)
     if state_out is not None:
         _expect("state_out", state_out, (B, H, d, dv), torch.float32, dev)
     elif return_state:
-        state_out = _new(on, stream, True, torch.empty, (B, H, d, dv), dtype=torch.float32, device=dev)
+        state_out = _empty(stream, (B, H, d, dv), torch.float32, dev)
+        if stream is not None:
+            state_out.record_stream(torch.cuda.current_stream(on))
     code = _CODES[q.dtype]
     if workspace is None:
         n = _bytes("hla_delta_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
-        workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, n, torch.uint8, dev)
     else:
         _given(workspace, dev, stream)
     _call(on, lib.hla_delta_forward, "hla_delta_forward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -227,7 +240,7 @@ def gated_delta_step(state, q, k, v, g, beta, scale: Optional[float] = None, out
             state.is_contiguous()):
         _expect("state", state, (B, H, d, dv), torch.float32, q.device)
     if out is None:
-        out = _new(on, stream, True, torch.empty_like, v)
+        out, = _likes(on, stream, v)
     else:
         _expect("out", out, tuple(v.shape), v.dtype, q.device)
     _call(on, _library().hla_delta_step, "hla_delta_step rejected the call", state.data_ptr(), q.data_ptr(),
@@ -262,11 +275,10 @@ def gated_delta_backward(q, k, v, g, beta, dout, scale: Optional[float] = None, 
         n = _bytes("hla_delta_backward_workspace_bytes", code, B, Hk, H, T, d, dv)
         if n == 0:
             raise HLAError(5, f"no gated delta kernel for B={B} Hk={Hk} H={H} T={T} d={d} dv={dv}")
-        workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, n, torch.uint8, dev)
     else:
         _given(workspace, dev, stream)
-    dq, dk, dvv, dg, dbeta = (_new(on, stream, True, torch.empty_like, t) for t in (q, k, v, g, beta))
-    dstate0 = _new(on, stream, True, torch.empty_like, initial_state) if initial_state is not None else None
+    dq, dk, dvv, dg, dbeta, dstate0 = _likes(on, stream, q, k, v, g, beta, initial_state)
     _call(on, lib.hla_delta_backward, "hla_delta_backward rejected the call", q.data_ptr(), k.data_ptr(), v.data_ptr(),
             g.data_ptr(), beta.data_ptr(), _ptr(initial_state), _ptr(lengths), dout.data_ptr(), _ptr(dstate),
             dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dstate0), B, Hk, H, T, d,
@@ -314,7 +326,7 @@ def group_norm(x, groups: int, weight=None, bias=None, gate=None, eps: float = 1
     C, rows, flags = _norm_args(x, groups, weight, bias, gate, activation, center)
     on = x.get_device()
     if out is None:
-        out = _new(on, stream, True, torch.empty_like, x)
+        out, = _likes(on, stream, x)
     else:
         _expect("out", out, tuple(x.shape), x.dtype, x.device)
     _call(on, _library().hla_group_norm_forward, "hla_group_norm_forward rejected the call", x.data_ptr(), _ptr(gate),
@@ -331,8 +343,7 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
     _expect("dy", dy, tuple(x.shape), x.dtype, x.device)
     on = x.get_device()
     lib = _library()
-    dx, dgate, dweight, dbias = (_new(on, stream, True, torch.empty_like, t) if t is not None else None
-                                 for t in (x, gate, weight, bias))
+    dx, dgate, dweight, dbias = _likes(on, stream, x, gate, weight, bias)
     nbytes = 0
     if workspace is not None:
         _given(workspace, x.device, stream)
@@ -341,7 +352,7 @@ def group_norm_backward(x, dy, groups: int, weight=None, bias=None, gate=None, e
             n = _bytes("hla_group_norm_backward_workspace_bytes", _CODES[x.dtype], rows, C, groups)
             if n == 0:
                 raise HLAError(5, f"no group norm kernel for {rows} rows of {C} channels in {groups} groups")
-            workspace = _new(on, stream, False, torch.empty, n, dtype=torch.uint8, device=x.device)
+            workspace = _empty(stream, n, torch.uint8, x.device)
         nbytes = workspace.numel() * workspace.element_size()
     _call(on, lib.hla_group_norm_backward, "hla_group_norm_backward rejected the call", x.data_ptr(), _ptr(gate),
             _ptr(weight), _ptr(bias), dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dweight), _ptr(dbias), rows, C,
