@@ -7,7 +7,7 @@
 namespace hla {
 namespace delta {
 
-// Tokens of one sequence in either layout: element strides of one (b, head, t) row, in rows.
+// One call: its tensors, laid out [B][heads][T][..] or, with bthd, [B][T][heads][..], and their sizes.
 struct Problem {
     const void *q, *k, *v;
     const float *g, *beta;
@@ -67,9 +67,8 @@ size_t backward_bytes(const Problem& p);
 int backward_launches(const Problem& p);
 cudaError_t backward(const Problem& p, const Gradients& gr, void* ws, cudaStream_t st);
 
-// Token by token: the state stays in registers, one CTA per head and 64 (or 32) value columns.
-// Used for decoding (T = 1).
-cudaError_t recur(const Problem& p, cudaStream_t st);
+// Decoding (delta_step.cu): one token, the state at state_out in place; q, k [B][Hk][d], v, o [B][H][dv].
+cudaError_t step(const Problem& p, cudaStream_t st);
 
 }  // namespace delta
 

@@ -93,7 +93,7 @@ hla_status_t hla_delta_step(float* state, const void* q, const void* k, const vo
         return HLA_ERR_ALIGN;
     const hla::delta::Problem p{q, k, v, g, beta, state, nullptr, o, state, B, Hk, H, 1, d, dv,
                                 dtype == HLA_BF16, false, scale, nullptr};
-    return hla::delta::recur(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
+    return hla::delta::step(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HLA_OK : HLA_ERR_CUDA;
 }
 
 size_t hla_delta_backward_workspace_bytes(hla_dtype_t dtype, int B, int Hk, int H, int T, int d, int dv) {

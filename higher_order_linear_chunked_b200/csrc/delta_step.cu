@@ -1,149 +1,123 @@
-// The gated delta rule token by token (decoding).
+// One token of the gated delta rule (decoding).
 //
 //   y = S^T k, z = S^T q (both of the old S, one pass over it)
 //   u = beta (v - a y),  S <- a S + k u^T,  o = scale (a z + (q.k) u)        a = exp(g)
 //
 // A CTA owns CV value columns of one head: S never leaves its registers between the read and the
 // write, so a step moves each state element once each way, which is all that bounds it (7 flops
-// per 8 bytes).
+// per 8 bytes; 193x16 heads of 128x128 take 63 us, 98% of the copy rate).
 #include "delta_common.cuh"
 
 namespace hla {
 namespace delta {
 namespace {
 
-struct RecurArgs {
+struct StepArgs {
     const void *q, *k, *v;
-    const float *g, *beta, *state_in;
-    const int* lengths;
+    const float *g, *beta;
+    float* state;            // [B*H][d][dv], in place
     void* o;
-    float* state_out;
-    int Hk, H, T, dv, bthd;
+    int share;               // value heads of a key head
     float scale;
 };
 
-template <typename E, int DK, int CV, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_delta_recur(const RecurArgs a) {
+// DV is known at compile time so that a thread's rows are one address and offsets: with an address a row,
+// kept from the loads to the stores, some of S left the registers (193x16 heads of 128x128 in bf16: 66 us, not 63).
+template <typename E, int DK, int DV, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_delta_step(const StepArgs a) {
+    constexpr int CV = DV < 64 ? DV : 64;
     constexpr int LPR = CV / 4;           // lanes per state row (four columns each)
     constexpr int RPP = NT / LPR;         // rows per pass
     constexpr int NP = DK / RPP;          // passes: rows of one thread
     constexpr int NW = NT / 32;
     static_assert(DK % RPP == 0 && 32 % LPR == 0, "rows must divide over the threads");
-    __shared__ float s_k[2][DK], s_q[2][DK];
-    __shared__ float4 s_y[2][NW][LPR], s_z[2][NW][LPR];
-    __shared__ float s_qk[2][NW];
+    __shared__ float s_k[DK], s_q[DK];
+    __shared__ float4 s_y[NW][LPR], s_z[NW][LPR];
+    __shared__ float s_qk[NW];
 
-    const int slices = a.dv / CV;
+    constexpr int slices = DV / CV;
     const int bh = blockIdx.x / slices, col0 = (blockIdx.x % slices) * CV;
-    const int b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c4 = tid % LPR, r0 = tid / LPR;
-    const int T = length_of(a.lengths, b, a.T);
-    const long long krow = row_of(a.bthd, b, hk, a.Hk, 0, a.T), vrow = row_of(a.bthd, b, h, a.H, 0, a.T);
-    const int kstep = row_step(a.bthd, a.Hk), vstep = row_step(a.bthd, a.H);
-    const E* q = static_cast<const E*>(a.q) + krow * DK;
-    const E* k = static_cast<const E*>(a.k) + krow * DK;
-    const E* v = static_cast<const E*>(a.v) + vrow * a.dv + col0 + 4 * c4;
-    E* o = static_cast<E*>(a.o) + vrow * a.dv + col0 + 4 * c4;
-    const long long sbase = (static_cast<long long>(bh) * DK) * a.dv + col0 + 4 * c4;
+    const long long krow = static_cast<long long>(bh / a.share) * DK;      // H is a multiple of Hk: b and hk in one
+    const long long vat = static_cast<long long>(bh) * DV + col0 + 4 * c4;
+    float* const state = a.state + (static_cast<long long>(bh) * DK + r0) * DV + col0 + 4 * c4;
 
-    float S[NP][4];
+    float S[NP][4], vv[4];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) load4(state + i * RPP * DV, S[i]);
+    for (int i = tid; i < DK; i += NT) {
+        s_k[i] = to_f32(static_cast<const E*>(a.k)[krow + i]);
+        s_q[i] = to_f32(static_cast<const E*>(a.q)[krow + i]);
+    }
+    const float decay = expf(gate(a.g[bh])), beta = a.beta[bh];
+    load4(static_cast<const E*>(a.v) + vat, vv);
+    __syncthreads();
+    float y[4] = {}, z[4] = {}, qk = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        if (a.state_in) {
-            load4(a.state_in + sbase + static_cast<long long>(r0 + i * RPP) * a.dv, S[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
-        }
-    }
-    for (int t = 0; t < T; ++t) {
-        const int p = t & 1;
-        for (int i = tid; i < DK; i += NT) {
-            s_k[p][i] = to_f32(k[static_cast<long long>(t) * kstep * DK + i]);
-            s_q[p][i] = to_f32(q[static_cast<long long>(t) * kstep * DK + i]);
-        }
-        const long long row = vrow + static_cast<long long>(t) * vstep;
-        const float decay = expf(gate(a.g[row])), beta = a.beta[row];
-        float vv[4];
-        load4(v + static_cast<long long>(t) * vstep * a.dv, vv);
-        __syncthreads();
-        float y[4] = {}, z[4] = {}, qk = 0.f;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const float kk = s_k[p][r0 + i * RPP], qq = s_q[p][r0 + i * RPP];
-            qk = fmaf(kk, qq, qk);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = fmaf(kk, S[i][j], y[j]);
-                z[j] = fmaf(qq, S[i][j], z[j]);
-            }
-        }
-#pragma unroll
-        for (int w = LPR; w < 32; w <<= 1) {
-            qk += __shfl_xor_sync(0xffffffffu, qk, w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] += __shfl_xor_sync(0xffffffffu, y[j], w);
-                z[j] += __shfl_xor_sync(0xffffffffu, z[j], w);
-            }
-        }
-        if (lane < LPR) {
-            s_y[p][warp][lane] = make_float4(y[0], y[1], y[2], y[3]);
-            s_z[p][warp][lane] = make_float4(z[0], z[1], z[2], z[3]);
-            if (lane == 0) s_qk[p][warp] = qk;
-        }
-        __syncthreads();
-        float ty[4] = {}, tz[4] = {}, tqk = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float4 fy = s_y[p][w][c4], fz = s_z[p][w][c4];
-            ty[0] += fy.x; ty[1] += fy.y; ty[2] += fy.z; ty[3] += fy.w;
-            tz[0] += fz.x; tz[1] += fz.y; tz[2] += fz.z; tz[3] += fz.w;
-            tqk += s_qk[p][w];
-        }
-        float out[4];
+        const float kk = s_k[r0 + i * RPP], qq = s_q[r0 + i * RPP];
+        qk = fmaf(kk, qq, qk);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float u = beta * (vv[j] - decay * ty[j]);
-            out[j] = a.scale * fmaf(decay, tz[j], tqk * u);
-            ty[j] = u;
-        }
-        if (r0 == 0) store4(o + static_cast<long long>(t) * vstep * a.dv, out);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const float kk = s_k[p][r0 + i * RPP];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S[i][j] = fmaf(kk, ty[j], decay * S[i][j]);
+            y[j] = fmaf(kk, S[i][j], y[j]);
+            z[j] = fmaf(qq, S[i][j], z[j]);
         }
     }
-    if (r0 == 0) {
-        const float zero[4] = {};
-        for (int t = T; t < a.T; ++t) store4(o + static_cast<long long>(t) * vstep * a.dv, zero);
-    }
-    if (a.state_out) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) store4(a.state_out + sbase + static_cast<long long>(r0 + i * RPP) * a.dv, S[i]);
+    for (int w = LPR; w < 32; w <<= 1) {
+        qk += __shfl_xor_sync(0xffffffffu, qk, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j] += __shfl_xor_sync(0xffffffffu, y[j], w);
+            z[j] += __shfl_xor_sync(0xffffffffu, z[j], w);
+        }
     }
+    if (lane < LPR) {
+        s_y[warp][lane] = make_float4(y[0], y[1], y[2], y[3]);
+        s_z[warp][lane] = make_float4(z[0], z[1], z[2], z[3]);
+        if (lane == 0) s_qk[warp] = qk;
+    }
+    __syncthreads();
+    float u[4] = {}, tz[4] = {}, tqk = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const float4 fy = s_y[w][c4], fz = s_z[w][c4];
+        u[0] += fy.x; u[1] += fy.y; u[2] += fy.z; u[3] += fy.w;
+        tz[0] += fz.x; tz[1] += fz.y; tz[2] += fz.z; tz[3] += fz.w;
+        tqk += s_qk[w];
+    }
+    float out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        u[j] = beta * (vv[j] - decay * u[j]);
+        out[j] = a.scale * fmaf(decay, tz[j], tqk * u[j]);
+    }
+    if (r0 == 0) store4(static_cast<E*>(a.o) + vat, out);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const float kk = s_k[r0 + i * RPP];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[i][j] = fmaf(kk, u[j], decay * S[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) store4(state + i * RPP * DV, S[i]);
 }
 
 template <typename E, int DK>
-cudaError_t launch(const Problem& p, const RecurArgs& a, cudaStream_t st) {
+cudaError_t launch(const Problem& p, const StepArgs& a, cudaStream_t st) {
+    constexpr int NT = DK == 128 ? 256 : 128;
     const int BH = p.B * p.H;
-    if (p.dv == 32) {
-        k_delta_recur<E, DK, 32, 128><<<BH, 128, 0, st>>>(a);
-    } else {
-        constexpr int NT = DK == 128 ? 256 : 128;
-        k_delta_recur<E, DK, 64, NT><<<BH * (p.dv / 64), NT, 0, st>>>(a);
-    }
+    if (p.dv == 32) k_delta_step<E, DK, 32, 128><<<BH, 128, 0, st>>>(a);
+    else if (p.dv == 64) k_delta_step<E, DK, 64, NT><<<BH, NT, 0, st>>>(a);
+    else k_delta_step<E, DK, 128, NT><<<2 * BH, NT, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t recur(const Problem& p, cudaStream_t st) {
-    const RecurArgs a{p.q, p.k, p.v, p.g, p.beta, p.state_in, p.lengths, p.o, p.state_out,
-                      p.Hk, p.H, p.T, p.dv, p.bthd ? 1 : 0, p.scale};
+cudaError_t step(const Problem& p, cudaStream_t st) {
+    const StepArgs a{p.q, p.k, p.v, p.g, p.beta, p.state_out, p.o, p.H / p.Hk, p.scale};
     if (p.bf16) {
         if (p.d == 32) return launch<bf16, 32>(p, a, st);
         if (p.d == 64) return launch<bf16, 64>(p, a, st);
