@@ -70,8 +70,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_reverse(cons
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = ptx::smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31;
-    // warp w runs on quarter w % 4 of an SM: the state warps on other quarters than the forward walk's
-    // state warps, beside which they run
     const int warp = tid >> 5;
     const int slices = a.dv / CS, walked = F::SUMMARY ? a.segments - 1 : a.segments;
     const int col0 = (blockIdx.x % slices) * CS, bh = blockIdx.x / slices / walked;
@@ -520,10 +518,9 @@ struct Blk {
     static constexpr int BLOCKS = DK <= 64 && bytes <= 113 * 1024 ? 2 : 1;
 };
 
-// R rows x D columns of fp32 (times fac[row] where given) into three swizzled bf16 terms.
+// R rows x D columns of fp32 into three swizzled bf16 terms.
 template <int RB, int R, int D, int NT>
-__device__ __forceinline__ void load_split(uint32_t tile, uint32_t term, const float* src, long long step, int rows, int tid,
-                                           const float* fac) {
+__device__ __forceinline__ void load_split(uint32_t tile, uint32_t term, const float* src, long long step, int rows, int tid) {
     constexpr int P = D / 4, U = 4;
 #pragma unroll 1
     for (int i0 = tid; i0 < R * P; i0 += NT * U) {
@@ -538,10 +535,9 @@ __device__ __forceinline__ void load_split(uint32_t tile, uint32_t term, const f
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * NT, r = i / P, c = i % P;
             if (i >= R * P) continue;
-            const float w = fac ? fac[r] : 1.f;
             uint32_t lo[3], hi[3];
-            split<3>(x[u].x * w, x[u].y * w, lo);
-            split<3>(x[u].z * w, x[u].w * w, hi);
+            split<3>(x[u].x, x[u].y, lo);
+            split<3>(x[u].z, x[u].w, hi);
 #pragma unroll
             for (int t = 0; t < 3; ++t)
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tile + t * term + piece<RB>(r, c >> 1) + (c & 1) * 8),
@@ -563,7 +559,7 @@ __device__ __forceinline__ void load_rows(uint32_t tile, const bf16* src, long l
 }
 template <int N, int D, int KT, int NT>
 __device__ __forceinline__ void load_rows(uint32_t tile, const float* src, long long step, int rows, int tid) {
-    load_split<D * 2, N, D, NT>(tile, N * D * 2, src, step, rows, tid, nullptr);
+    load_split<D * 2, N, D, NT>(tile, N * D * 2, src, step, rows, tid);
 }
 
 // sum over this lane's columns of acc[row] * tile[row], rows r0 + lane / 4 (+ 8); all four lanes get it
