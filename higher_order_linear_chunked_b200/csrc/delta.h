@@ -42,6 +42,8 @@ struct Segments {
 Segments segments(const Problem& p, bool gradients);
 // Value columns of a block of the gradients' two walks over `walked` heads (times segments).
 int gradient_columns(const Problem& p, long long walked);
+// Whether those two walks, of `blocks` blocks each, run side by side.
+bool gradient_walks_beside(const Problem& p, long long blocks);
 // The states between the segments, from the first on: sums [BH][count - 1][d][dv | d] holds (B | A) of
 // every segment but the last (the first one's B from the given state), first the given state or null.
 // With back: from the last on, S = A^T S' + back [BH][count][d][dv].  out: [BH][count][d][dv].

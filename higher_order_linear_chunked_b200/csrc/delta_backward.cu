@@ -1061,14 +1061,16 @@ Space space(const Problem& p) {
 }
 
 template <typename F>
-cudaError_t start(const ReverseArgs& a, int blocks, cudaStream_t st) {
+cudaError_t start(const ReverseArgs& a, bool beside, int blocks, cudaStream_t st) {
     static_assert(F::bytes <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = allow_smem<k_delta_reverse<F>>(F::bytes);
     if (e != cudaSuccess) return e;
-    return launch_beside(k_delta_reverse<F>, blocks, F::WARPS * 32, F::bytes, st, a);
+    if (beside) return launch_beside(k_delta_reverse<F>, blocks, F::WARPS * 32, F::bytes, st, a);
+    k_delta_reverse<F><<<blocks, F::WARPS * 32, F::bytes, st>>>(a);
+    return cudaGetLastError();
 }
 
-// The two walks.  Neither needs the other, so the reverse walk runs beside the forward one, and so do
+// The two walks.  Neither needs the other, so the reverse walk mostly runs beside the forward one, and so do
 // their summaries and folds where there are segments (the linear part of a segment backwards is the
 // transpose of the forward walk's A).  4x16x4096x64 in bf16 222 us, one after the other 314; fp32
 // 2x8x4096x32 (in segments) all gradients 169 and 205, 2x16x512x32 50 and 68.
@@ -1089,7 +1091,7 @@ cudaError_t walks(const Problem& p, const Gradients& gr, char* ws, const Space& 
         float* sums = reinterpret_cast<float*>(ws + s.sums);
         float* starts = reinterpret_cast<float*>(ws + s.starts);
         e = summarize(p, g, records, sums, st);
-        if (e == cudaSuccess) e = start<Rev<E, DK, NG, true>>(a, BH * (g.count - 1) * slices, st);
+        if (e == cudaSuccess) e = start<Rev<E, DK, NG, true>>(a, true, BH * (g.count - 1) * slices, st);
         if (e == cudaSuccess) e = fold(p, g, sums, nullptr, p.state_in, starts, st);
         if (e == cudaSuccess) e = fold(p, g, sums, back, gr.dstate_out, behind, st);
         a.behind = behind;
@@ -1100,8 +1102,9 @@ cudaError_t walks(const Problem& p, const Gradients& gr, char* ws, const Space& 
                          block_tokens(p) / C, st);
     if (e != cudaSuccess) return e;
     if constexpr (sizeof(E) == 2 && DK <= 64)
-        if (gradient_columns(p, static_cast<long long>(p.B) * p.H * g.count) == 64) return start<Rev<E, DK, 4, false>>(a, BH * g.count * (p.dv / 64), st);
-    return start<Rev<E, DK, NG, false>>(a, BH * g.count * slices, st);
+        if (gradient_columns(p, static_cast<long long>(p.B) * p.H * g.count) == 64) return start<Rev<E, DK, 4, false>>(a, true, BH * g.count * (p.dv / 64), st);
+    const int blocks = BH * g.count * slices;
+    return start<Rev<E, DK, NG, false>>(a, gradient_walks_beside(p, blocks), blocks, st);
 }
 
 template <typename E, int DK, int DV>

@@ -120,6 +120,15 @@ int gradient_columns(const Problem& p, long long walked) {
     return p.d <= 64 && p.dv % 64 == 0 && walks * (p.dv / 32) > kSMs && walks * (p.dv / 64) <= kSMs ? 64 : 32;
 }
 
+// Side by side the walks are faster or the same for all widths and types (bf16 5x8x2048x128: 668 us, one after
+// the other 728; fp32 16x16x512x32: 232 and 252), but not for bf16 with d = 64 where one walk alone has a
+// block or two for every SM: two reverse blocks leave an SM no room for a forward one, and the second walk's
+// last blocks come late (5x16x2048x64: 504 us, one after the other 471; 9x16x1024x64 360 and 337; 8x16x2048x64
+// 639 and 606; with more blocks the same again, 16x16x1024x64 574 and 575).
+bool gradient_walks_beside(const Problem& p, long long blocks) {
+    return !(p.bf16 && p.d == 64 && blocks > kSMs && blocks <= 2 * kSMs);
+}
+
 // Steps of chunks one after another, in units of one walk step: without segments, all chunks of a head
 // as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
 // takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step, two
