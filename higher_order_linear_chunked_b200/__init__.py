@@ -25,6 +25,7 @@ bf16 tensors; the output is fp32 ``[B, H, T, dv]``.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
@@ -479,8 +480,8 @@ _DELTA = ("gated_delta", "gated_delta_step", "gated_delta_backward", "gated_delt
 
 def __getattr__(name):
     # the delta module needs torch at import time; the rest of this module imports it when called
-    if name in _DELTA:
-        from . import delta
+    if name in _DELTA or name == "delta":
+        delta = importlib.import_module(".delta", __name__)        # becomes an attribute of this module too
         globals().update({n: getattr(delta, n) for n in _DELTA})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

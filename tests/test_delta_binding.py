@@ -1,4 +1,7 @@
 """What the Python calls over include/hla_delta.h check and allocate, on tensors without memory (no GPU)."""
+import os
+import subprocess
+import sys
 from types import SimpleNamespace
 
 import pytest
@@ -103,3 +106,9 @@ def test_what_a_call_on_a_given_stream_allocates(name, monkeypatch):
         watch.made.clear(), watch.kept.clear()
         call()
         assert watch.made and all(s is watch.current for _, s in watch.made) and not watch.kept
+
+
+def test_the_module_is_an_attribute_of_the_package():
+    """Without an import of it, and before any of its calls was used."""
+    code = "import higher_order_linear_chunked_b200 as hla; assert hla.delta.gated_delta is hla.gated_delta"
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
