@@ -14,6 +14,8 @@
 // sequence is cut into segments (delta_fold.cu): a first walk takes each segment from a zero state and
 // also takes the unit matrix through it without values, which gives S_end = A S_start + B; the states
 // between the segments follow from those, and the second walk has all segments at once.
+#include <type_traits>
+
 #include "delta_walk.cuh"
 
 namespace hla {
@@ -36,6 +38,12 @@ struct WalkArgs {
     int Hk, H, T, dv, bthd;
     int segments, seg_chunks; // chunks of a segment
     float scale;
+};
+
+// From which token of a chunk (of a half of it, with two state warps) the columns of a group are NaN.
+struct Bad {
+    int any, pad[3];
+    int first[16];
 };
 
 // GR: the records have the gradients' form.
@@ -78,11 +86,28 @@ struct Cfg {
     static constexpr int ex = uf + (MODE_ == OUT ? 2 * UB : 0);
     static constexpr int yf = ex + (NH > 1 ? W_STATE * 2048 : 0);    // Y of the chunk as an A operand; the decayed U
     static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
-    static constexpr int bytes = yf + (NH > 1 ? NG_ * YB : 0);
+    static constexpr int bf = yf + (NH > 1 ? NG_ * YB : 0);           // of the last two chunks for the outputs
+    static constexpr int bytes = bf + (MODE_ == OUT ? 2 * W_STATE * static_cast<int>(sizeof(Bad)) : 0);
     // of an SM; summaries of narrow bf16 heads are four warps and 38 kB, so that 128 registers a thread let
     // four share one (1x4x16384x64: 110 us, with three 126)
     static constexpr int BLOCKS = MODE_ == SUMMARY && BF && DK_ <= 64 ? 4 : bytes <= 113 * 1024 ? 2 : 1;
 };
+
+// The first bad token of a warp's writes beta R, column by column, for the outputs.
+template <int N>
+__device__ __forceinline__ void tell(Bad* to, const float (&r)[N][4], const float2 (&beta)[N], int lane) {
+    float u[N][4];
+    int first[2];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[n][j] = r[n][j] * ((j & 1) ? beta[n].y : beta[n].x);
+    first_bad(u, lane, first);
+    if ((lane & 3) == 0) {
+        to->first[lane >> 2] = first[0];
+        to->first[8 + (lane >> 2)] = first[1];
+    }
+}
 
 template <typename F>
 __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const WalkArgs a) {
@@ -150,6 +175,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
             const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates + gstage * 512);
             uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 16) + part * (DH / 16)) * OT * 32 + lane;
             uint2* uf = reinterpret_cast<uint2*>(sm + F::uf + (c & 1) * F::UB) + grp * 2 * OT * 64 + lane * 2;
+            Bad* const bf = reinterpret_cast<Bad*>(sm + F::bf) + (c & 1) * F::W_STATE + warp;
             if (MODE == STORE) {
                 const int chunk = t_first / C + c;
                 if (chunk % a.block_chunks == 0) {
@@ -194,9 +220,13 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 }
                 // R^T = Y^T X^T; X is lower triangular
                 const uint32_t x_n = at_pieces_first<C * 2>(sb + F::x + so, 0, 0, lane);
-                float r[4][4] = {};
-                {
+                float r[4][4];
+                const auto solve = [&] {
                     uint32_t ay[3][4], bx[2][3][4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[n][j] = 0.f;
 #pragma unroll
                     for (int np = 0; np < 2; ++np)
 #pragma unroll
@@ -207,6 +237,23 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     for (int t = 0; t < 3; ++t) ldsm4(bx[0][t], (x_n ^ 32) + t * (C * C * 2) + 16 * C * 2);
                     split_a<3>(y[2], y[3], ay);
                     prod2<3, 3>(r[2], r[3], ay, bx[0]);
+                };
+                solve();
+                float2 be[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) be[n] = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
+                if constexpr (MODE == OUT) {
+                    // found while the products are under way; then once more, cleaned
+                    const bool spoilt = any_bad(y) || G->bad != 0.f;
+                    if (lane == 0) bf->any = spoilt;
+                    if (spoilt) {
+                        int first[2];
+                        first_bad(y, lane, first);
+                        clean(y);
+                        solve();
+                        spoil(r, lane, first);
+                        tell(bf, r, be, lane);
+                    }
                 }
                 if (MODE == STORE) {
 #pragma unroll
@@ -224,9 +271,8 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                     for (int n = 2 * kk; n < 2 * kk + 2; ++n) {
-                        const float2 be = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? be.y : be.x;
+                        for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? be[n].y : be[n].x;
                     }
                     if (MODE == OUT) {
                         uint32_t ao[OT][4];
@@ -305,6 +351,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     for (int j = 0; j < 4; ++j) mine[n % TN][j] = y[n][j];
             ptx::named_sync(1 + grp, NH * 32);
             // Y^T = V^T - (S0^T K^T) e^c for the tokens of this part
+            float z[TN][4];
 #pragma unroll
             for (int e = 0; e < TN; ++e) {
                 const int n = part * TN + e;
@@ -314,15 +361,11 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     const float4 x = ex[((part ^ o) * 4 + n) * 32];
                     w[0] += x.x; w[1] += x.y; w[2] += x.z; w[3] += x.w;
                 }
-                float z[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float vv = TN == 2 ? v[e][j] : ((part & 1) ? v[1][j] : v[0][j]);
-                    z[j] = fmaf((j & 1) ? -since[e].y : -since[e].x, w[j], vv);
-                }
+                for (int j = 0; j < 4; ++j) z[e][j] = fmaf((j & 1) ? -since[e].y : -since[e].x, w[j], v[e][j]);
                 uint32_t t0[3], t1[3];
-                split<3>(z[0], z[1], t0);
-                split<3>(z[2], z[3], t1);
+                split<3>(z[e][0], z[e][1], t0);
+                split<3>(z[e][2], z[e][3], t1);
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
                     reinterpret_cast<uint2*>(yf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
@@ -337,6 +380,8 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     const uint4 u = reinterpret_cast<const uint4*>(yf)[(kk * 3 + t) * 32 + lane];
                     ay[kk][t][0] = u.x; ay[kk][t][1] = u.y; ay[kk][t][2] = u.z; ay[kk][t][3] = u.w;
                 }
+            float u[TN][4];
+            const auto solve = [&] {
 #pragma unroll
             for (int e = 0; e < TN; ++e) {
                 const int n = part * TN + e;
@@ -348,29 +393,56 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                         mma16816(r[(i + j) & 1], ay[0][i], bx[e][j][0], bx[e][j][1]);
                         if (n >= 2) mma16816(r[2 + ((i + j) & 1)], ay[1][i], bx[e][j][2], bx[e][j][3]);
                     }
-                // U^T for the outputs, and U^T e^(c_C - c) for the state
-                float u[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = (r[0][j] + r[1][j]) + (r[2][j] + r[3][j]);
-                if (MODE == STORE) {
+                for (int j = 0; j < 4; ++j) u[e][j] = (r[0][j] + r[1][j]) + (r[2][j] + r[3][j]);
+            }
+            };
+            solve();
+            if (MODE == STORE) {
+#pragma unroll
+                for (int e = 0; e < TN; ++e) {
+                    const int n = part * TN + e;
                     const int tok = t_first + c * C + 8 * n + 2 * (lane & 3);
                     float* to = a.errors + (static_cast<long long>(bh) * a.T + tok) * a.dv + col0 + 16 * grp + (lane >> 2);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (tok + (j & 1) < t_end) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[j];
+                        if (tok + (j & 1) < t_end) to[(j & 1) * a.dv + 8 * (j >> 1)] = u[e][j];
                 }
+            }
+            if constexpr (MODE == OUT) {
+                const bool spoilt = any_bad(u) || G->bad != 0.f;
+                if (lane == 0) bf->any = spoilt;
+                if (spoilt) {
+                    // once more with this half's share cleaned; the other half's stays as it is, since all of this
+                    // half comes behind what is bad there
+                    int first[2];
+                    first_bad(z, lane, first);
+                    clean(z);
+                    if (part == 0) split_a<3>(z[0], z[1], ay[0]);
+                    else split_a<3>(z[0], z[1], ay[1]);
+                    solve();
+                    spoil(u, lane, first);
+                    tell(bf, u, beta, lane);
+                }
+            }
+            // U^T for the outputs, and U^T e^(c_C - c) for the state
 #pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] *= (j & 1) ? beta[e].y : beta[e].x;
+            for (int e = 0; e < TN; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[e][j] *= (j & 1) ? beta[e].y : beta[e].x;
+#pragma unroll
+            for (int e = 0; e < TN; ++e) {
+                const int n = part * TN + e;
                 uint32_t t0[3], t1[3];
-                split<3>(u[0] * left[e].x, u[1] * left[e].y, t0);
-                split<3>(u[2] * left[e].x, u[3] * left[e].y, t1);
+                split<3>(u[e][0] * left[e].x, u[e][1] * left[e].y, t0);
+                split<3>(u[e][2] * left[e].x, u[e][3] * left[e].y, t1);
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
                     reinterpret_cast<uint2*>(vf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
                 if (MODE == OUT) {
                     uint32_t o0[OT], o1[OT];
-                    split<OT>(u[0], u[1], o0);
-                    split<OT>(u[2], u[3], o1);
+                    split<OT>(u[e][0], u[e][1], o0);
+                    split<OT>(u[e][2], u[e][3], o1);
 #pragma unroll
                     for (int t = 0; t < OT; ++t) uf[((n >> 1) * OT + t) * 64 + (n & 1)] = make_uint2(o0[t], o1[t]);
                 }
@@ -424,43 +496,68 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
             const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 16) * OT * 32 + lane;
             const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + (c & 1) * F::UB) + g * 2 * OT * 32 + lane;
             float acc[2][2][4] = {};          // [16 tokens][8 columns]
+            const auto chunk = [&](auto with_bad) {
+                constexpr bool spoilt = decltype(with_bad)::value;
 #pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-                uint32_t aq[2][KT][4], bs[1][OT][4];
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    uint32_t aq[2][KT][4], bs[1][OT][4];
 #pragma unroll
-                for (int t = 0; t < OT; ++t) {
-                    const uint4 u = sf[(ks * OT + t) * 32];
-                    bs[0][t][0] = u.x; bs[0][t][1] = u.z; bs[0][t][2] = u.y; bs[0][t][3] = u.w;
+                    for (int t = 0; t < OT; ++t) {
+                        const uint4 u = sf[(ks * OT + t) * 32];
+                        bs[0][t][0] = u.x; bs[0][t][1] = u.z; bs[0][t][2] = u.y; bs[0][t][3] = u.w;
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                        for (int t = 0; t < KT; ++t) ldsm4(aq[m][t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2) + m * 16 * DK * 2);
+                        prod<KT, OT, 1>(acc[m], aq[m], bs);
+                    }
                 }
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
+                    const float f[2] = {a.scale * G->since[16 * m + (lane >> 2)], a.scale * G->since[16 * m + 8 + (lane >> 2)]};
 #pragma unroll
-                    for (int t = 0; t < KT; ++t) ldsm4(aq[m][t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2) + m * 16 * DK * 2);
-                    prod<KT, OT, 1>(acc[m], aq[m], bs);
-                }
-            }
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float f[2] = {a.scale * G->since[16 * m + (lane >> 2)], a.scale * G->since[16 * m + 8 + (lane >> 2)]};
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[m][n][j] *= f[j >> 1];
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                uint32_t ap[OT][4], bu[1][OT][4];
-#pragma unroll
-                for (int t = 0; t < OT; ++t) {
-                    const uint4 u = uf[(kk * OT + t) * 32];
-                    bu[0][t][0] = u.x; bu[0][t][1] = u.z; bu[0][t][2] = u.y; bu[0][t][3] = u.w;
+                        for (int j = 0; j < 4; ++j) acc[m][n][j] *= f[j >> 1];
                 }
 #pragma unroll
-                for (int m = kk; m < 2; ++m) {     // P is lower triangular
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint32_t ap[OT][4], bu[1][OT][4];
 #pragma unroll
-                    for (int t = 0; t < OT; ++t) ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2) + m * 16 * C * 2);
-                    prod<OT, OT, 1>(acc[m], ap, bu);
+                    for (int t = 0; t < OT; ++t) {
+                        const uint4 u = uf[(kk * OT + t) * 32];
+                        bu[0][t][0] = u.x; bu[0][t][1] = u.z; bu[0][t][2] = u.y; bu[0][t][3] = u.w;
+                        if constexpr (spoilt) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) bu[0][t][j] = clean_pair(bu[0][t][j]);
+                        }
+                    }
+#pragma unroll
+                    for (int m = kk; m < 2; ++m) {     // P is lower triangular
+#pragma unroll
+                        for (int t = 0; t < OT; ++t) ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2) + m * 16 * C * 2);
+                        prod<OT, OT, 1>(acc[m], ap, bu);
+                    }
                 }
+            };
+            const Bad* const bf = reinterpret_cast<const Bad*>(sm + F::bf) + (c & 1) * F::W_STATE + g * NH;
+            if ((bf[0].any | bf[NH - 1].any) == 0) {
+                chunk(std::false_type{});
+            } else {
+                chunk(std::true_type{});
+#pragma unroll
+                for (int part = 0; part < NH; ++part)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            int first = bf[part].any ? bf[part].first[8 * n + 2 * (lane & 3) + (j & 1)] : C;
+                            if (NH > 1) first = first < 16 ? first + 16 * part : C;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+                                if (16 * m + (lane >> 2) + 8 * (j >> 1) >= first) acc[m][n][j] = __int_as_float(0x7fffffff);
+                        }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

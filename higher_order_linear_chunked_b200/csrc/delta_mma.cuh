@@ -136,6 +136,56 @@ __device__ __forceinline__ void split_a(const float (&lo)[4], const float (&hi)[
     for (int i = 0; i < N; ++i) a[i][3] = t[i];
 }
 
+// A NaN or an infinity of one token must not reach the tokens before it, but 0 x NaN is NaN, and the
+// triangular products multiply every token of a 16 x 16 block with the zeros above the diagonal.  Where a
+// warp finds such a value in the tokens' axis of an operand (x: accumulator tiles, tile n's tokens
+// 8 n + 2 (lane % 4) + (j & 1), columns lane / 4 + 8 (j >> 1)), it takes the product of the cleaned operand
+// and makes NaN of the tokens from the first bad one on, column by column.
+template <int N>
+__device__ __forceinline__ bool any_bad(const float (&x)[N][4]) {       // of the warp's: 0 x is NaN then
+    float s[4] = {};
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = fmaf(x[n][j], 0.f, s[j]);
+    return __any_sync(0xffffffffu, (s[0] + s[1]) + (s[2] + s[3]) != 0.f);
+}
+__device__ __forceinline__ bool bad(float x) { return !(fabsf(x) <= 3.4028235e38f); }
+template <int N>
+__device__ __forceinline__ void first_bad(const float (&x)[N][4], int lane, int (&first)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int f = 8 * N;
+#pragma unroll
+        for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+            for (int j = 1; j >= 0; --j)
+                if (bad(x[n][2 * h + j])) f = 8 * n + 2 * (lane & 3) + j;
+        f = min(f, __shfl_xor_sync(0xffffffffu, f, 1));
+        first[h] = min(f, __shfl_xor_sync(0xffffffffu, f, 2));
+    }
+}
+template <int N>
+__device__ __forceinline__ void clean(float (&x)[N][4]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = bad(x[n][j]) ? 0.f : x[n][j];
+}
+__device__ __forceinline__ uint32_t clean_pair(uint32_t x) {           // two bf16 terms
+    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+    return x;
+}
+template <int N>
+__device__ __forceinline__ void spoil(float (&x)[N][4], int lane, const int (&first)[2]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (8 * n + 2 * (lane & 3) + (j & 1) >= first[j >> 1]) x[n][j] = __int_as_float(0x7fffffff);
+}
+
 // Byte offset of 16-byte piece c of row r in a bf16 tile with rows of RB bytes, swizzled so that
 // eight rows of one piece (an ldmatrix) and eight pieces of one row fall on all banks.
 template <int RB>

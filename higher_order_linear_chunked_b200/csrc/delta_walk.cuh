@@ -56,7 +56,8 @@ constexpr int kMS = 36;                      // floats of a row of the transpose
 struct Gates {
     float since[C], left[C], beta[C];
     float all;
-    float pad[31];
+    float bad;               // not 0: a beta is infinite or NaN
+    float pad[30];
 };
 static_assert(sizeof(Gates) == 512, "a record's last piece");
 
@@ -190,7 +191,9 @@ __device__ __forceinline__ void finish_gates(Gates* s, float2* sum, float g, flo
     s->since[lane] = since;
     s->left[lane] = ex2_long(last - c);
     s->beta[lane] = beta;
-    s->pad[lane < 31 ? lane : 30] = 0.f;
+    s->pad[lane < 30 ? lane : 29] = 0.f;
+    const bool any = __any_sync(0xffffffffu, bad(beta));
+    if (lane == 0) s->bad = any ? 1.f : 0.f;
     if (lane == 31) s->all = since;
 }
 
@@ -306,12 +309,19 @@ __device__ __forceinline__ void invert(const float* mt, uint8_t* xt, int lane) {
     }
     float z[2][4] = {};
     prod2<3, 3>(z[0], z[1], a, b);
+    const bool spoilt = any_bad(z);
+    int first[2];
+    if (spoilt) {
+        first_bad(z, lane, first);
+        clean(z);
+    }
     // X21^T [col][i] = -Z^T X22^T
     split_a<3>(z[0], z[1], a);
 #pragma unroll
     for (int t = 0; t < 3; ++t) ldsm4(b[t], at_pieces_first<C * 2>(xb + t * TERM, 16, 2, lane));
     float y[2][4] = {};
     prod2<3, 3>(y[0], y[1], a, b);
+    if (spoilt) spoil(y, lane, first);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
