@@ -78,11 +78,12 @@ struct Cfg {
     static constexpr int behind = gates + NG_STAGES * 512;
     static constexpr int q = 0, p = q + KTILE;
     static constexpr int OSTAGE = MODE_ == OUT ? p + kXBytes : 0;
-    // S0 and U of the last two chunks for the outputs, the partial sums
+    // S0 and U of the last two chunks for the outputs (fp32: the output warps, which have the time, split
+    // them), the partial sums
     static constexpr int sf = behind + NS * OSTAGE;
-    static constexpr int SB = NG_ * (DK_ / 16) * OT * 512;
+    static constexpr int SB = NG_ * (DK_ / 8) * 512;
     static constexpr int uf = sf + (MODE_ == OUT ? 2 * SB : 0);
-    static constexpr int UB = NG_ * 2 * OT * 512;
+    static constexpr int UB = NG_ * 4 * 512;
     static constexpr int ex = uf + (MODE_ == OUT ? 2 * UB : 0);
     static constexpr int yf = ex + (NH > 1 ? W_STATE * 2048 : 0);    // Y of the chunk as an A operand; the decayed U
     static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
@@ -106,6 +107,20 @@ __device__ __forceinline__ void tell(Bad* to, const float (&r)[N][4], const floa
     if ((lane & 3) == 0) {
         to->first[lane >> 2] = first[0];
         to->first[8 + (lane >> 2)] = first[1];
+    }
+}
+
+// Two neighbouring tiles of S0 or U, transposed as the state warps hold them, as a B operand.
+template <bool CLEAN, int N>
+__device__ __forceinline__ void operand(const float4* from, uint32_t (&b)[N][4]) {
+    const float4 x = from[0], y = from[32];
+    float w[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
+    if constexpr (CLEAN) clean(w);
+    uint32_t a[N][4];
+    split_a<N>(w[0], w[1], a);
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        b[t][0] = a[t][0]; b[t][1] = a[t][2]; b[t][2] = a[t][1]; b[t][3] = a[t][3];
     }
 }
 
@@ -173,8 +188,12 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         for (int c = 0; c < chunks; ++c) {
             const uint32_t so = stage * F::STAGE;
             const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates + gstage * 512);
-            uint4* sf = reinterpret_cast<uint4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 16) + part * (DH / 16)) * OT * 32 + lane;
-            uint2* uf = reinterpret_cast<uint2*>(sm + F::uf + (c & 1) * F::UB) + grp * 2 * OT * 64 + lane * 2;
+            float4* const sf = reinterpret_cast<float4*>(sm + F::sf + (c & 1) * F::SB) + (grp * (DK / 8) + part * (DH / 8)) * 32 + lane;
+            float4* const uf = reinterpret_cast<float4*>(sm + F::uf + (c & 1) * F::UB) + grp * 4 * 32 + lane;
+            if (MODE == OUT) {
+#pragma unroll
+                for (int n = 0; n < DH / 8; ++n) sf[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
+            }
             Bad* const bf = reinterpret_cast<Bad*>(sm + F::bf) + (c & 1) * F::W_STATE + warp;
             if (MODE == STORE) {
                 const int chunk = t_first / C + c;
@@ -201,10 +220,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                             ldsm4(bk[np][t], ((k_n + so) ^ (ks << 5)) + t * (C * DK * 2) + np * 16 * DK * 2);
                     split_a<3>(S[2 * ks], S[2 * ks + 1], as);
                     prod<3, KT, 2>(y, as, bk);
-                    if (MODE == OUT) {
-#pragma unroll
-                        for (int t = 0; t < OT; ++t) sf[(ks * OT + t) * 32] = make_uint4(as[t][0], as[t][1], as[t][2], as[t][3]);
-                    }
                 }
                 // Y^T = V^T - (S0^T K^T) e^c
                 float v[4][4] = {};
@@ -275,11 +290,8 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                         for (int j = 0; j < 4; ++j) r[n][j] *= (j & 1) ? be[n].y : be[n].x;
                     }
                     if (MODE == OUT) {
-                        uint32_t ao[OT][4];
-                        split_a<OT>(r[2 * kk], r[2 * kk + 1], ao);
 #pragma unroll
-                        for (int t = 0; t < OT; ++t)
-                            reinterpret_cast<uint4*>(uf - lane * 2)[(kk * OT + t) * 32 + lane] = make_uint4(ao[t][0], ao[t][1], ao[t][2], ao[t][3]);
+                        for (int n = 2 * kk; n < 2 * kk + 2; ++n) uf[n * 32] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
                     }
 #pragma unroll
                     for (int n = 2 * kk; n < 2 * kk + 2; ++n) {
@@ -319,10 +331,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 uint32_t as[3][4];
                 split_a<3>(S[2 * ks], S[2 * ks + 1], as);
                 prod<3, KT, 2>(y, as, bk);
-                if (MODE == OUT) {
-#pragma unroll
-                    for (int t = 0; t < OT; ++t) sf[(ks * OT + t) * 32] = make_uint4(as[t][0], as[t][1], as[t][2], as[t][3]);
-                }
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -439,13 +447,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
                     reinterpret_cast<uint2*>(vf)[((n >> 1) * 3 + t) * 64 + lane * 2 + (n & 1)] = make_uint2(t0[t], t1[t]);
-                if (MODE == OUT) {
-                    uint32_t o0[OT], o1[OT];
-                    split<OT>(u[e][0], u[e][1], o0);
-                    split<OT>(u[e][2], u[e][3], o1);
-#pragma unroll
-                    for (int t = 0; t < OT; ++t) uf[((n >> 1) * OT + t) * 64 + (n & 1)] = make_uint2(o0[t], o1[t]);
-                }
+                if (MODE == OUT) uf[n * 32] = make_float4(u[e][0], u[e][1], u[e][2], u[e][3]);
             }
             uint32_t bt[2][DH / 16][KT][4];
             if constexpr (KT == 1) {
@@ -493,19 +495,14 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         for (int c = 0; c < chunks; ++c) {
             const uint32_t so = ostage * F::OSTAGE;
             const Gates* G = reinterpret_cast<const Gates*>(sm + F::gates + gstage * 512);
-            const uint4* sf = reinterpret_cast<const uint4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 16) * OT * 32 + lane;
-            const uint4* uf = reinterpret_cast<const uint4*>(sm + F::uf + (c & 1) * F::UB) + g * 2 * OT * 32 + lane;
+            const float4* sf = reinterpret_cast<const float4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 8) * 32 + lane;
+            const float4* uf = reinterpret_cast<const float4*>(sm + F::uf + (c & 1) * F::UB) + g * 4 * 32 + lane;
             float acc[2][2][4] = {};          // [16 tokens][8 columns]
             const auto chunk = [&](auto with_bad) {
-                constexpr bool spoilt = decltype(with_bad)::value;
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     uint32_t aq[2][KT][4], bs[1][OT][4];
-#pragma unroll
-                    for (int t = 0; t < OT; ++t) {
-                        const uint4 u = sf[(ks * OT + t) * 32];
-                        bs[0][t][0] = u.x; bs[0][t][1] = u.z; bs[0][t][2] = u.y; bs[0][t][3] = u.w;
-                    }
+                    operand<false>(sf + 2 * ks * 32, bs[0]);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
 #pragma unroll
@@ -524,15 +521,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     uint32_t ap[OT][4], bu[1][OT][4];
-#pragma unroll
-                    for (int t = 0; t < OT; ++t) {
-                        const uint4 u = uf[(kk * OT + t) * 32];
-                        bu[0][t][0] = u.x; bu[0][t][1] = u.z; bu[0][t][2] = u.y; bu[0][t][3] = u.w;
-                        if constexpr (spoilt) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) bu[0][t][j] = clean_pair(bu[0][t][j]);
-                        }
-                    }
+                    operand<decltype(with_bad)::value>(uf + 2 * kk * 32, bu[0]);
 #pragma unroll
                     for (int m = kk; m < 2; ++m) {     // P is lower triangular
 #pragma unroll
@@ -586,15 +575,9 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
         const E* vp = static_cast<const E*>(a.v) + vrow * a.dv + col0;
         constexpr int REC = record_bytes(F::INV);
         const uint8_t* rec = a.records + (static_cast<long long>(bh) * ((a.T + C - 1) / C) + t_first / C) * REC;
+        const uint8_t* behind = rec;
         int stage = 0, ostage = 0, gstage = 0;
         for (int c = 0; c <= chunks + F::AHEAD; ++c) {
-            if (MODE == OUT && c > 0 && c <= chunks) {      // queries and P of the chunk before
-                const uint32_t so = sb + F::behind + ostage * F::OSTAGE;
-                load_bytes<kXBytes, LT>(so + F::p, rec - REC + F::INV * kXBytes, lt);
-                load_tile<DK, KT, LT>(so + F::q, qp, ks, min(C, t_end - t_first - (c - 1) * C), lt);
-                qp += C * ks;
-                if (++ostage == F::NS) ostage = 0;
-            }
             if (c < chunks) {
                 const uint32_t sg = sb + stage * F::STAGE;
                 const int rows = min(C, t_end - t_first - c * C);
@@ -606,6 +589,13 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 rec += REC;
                 if (++stage == F::NS) stage = 0;
                 if (++gstage == F::NG_STAGES) gstage = 0;
+            }
+            if (MODE == OUT && c > 0 && c <= chunks) {      // queries and P of the chunk before
+                const uint32_t so = sb + F::behind + ostage * F::OSTAGE;
+                load_bytes<kXBytes, LT>(so + F::p, behind + F::INV * kXBytes, lt);
+                load_tile<DK, KT, LT>(so + F::q, qp, ks, min(C, t_end - t_first - (c - 1) * C), lt);
+                qp += C * ks; behind += REC;
+                if (++ostage == F::NS) ostage = 0;
             }
             cp_commit();
             cp_wait<F::AHEAD - 1>();

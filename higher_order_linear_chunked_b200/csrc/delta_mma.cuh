@@ -172,11 +172,6 @@ __device__ __forceinline__ void clean(float (&x)[N][4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[n][j] = bad(x[n][j]) ? 0.f : x[n][j];
 }
-__device__ __forceinline__ uint32_t clean_pair(uint32_t x) {           // two bf16 terms
-    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
-    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
-    return x;
-}
 template <int N>
 __device__ __forceinline__ void spoil(float (&x)[N][4], int lane, const int (&first)[2]) {
 #pragma unroll
