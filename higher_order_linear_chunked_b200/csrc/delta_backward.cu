@@ -1072,8 +1072,8 @@ cudaError_t start(const ReverseArgs& a, bool beside, int blocks, cudaStream_t st
 
 // The two walks.  Neither needs the other, so the reverse walk mostly runs beside the forward one, and so do
 // their summaries and folds where there are segments (the linear part of a segment backwards is the
-// transpose of the forward walk's A).  4x16x4096x64 in bf16 222 us, one after the other 314; fp32
-// 2x8x4096x32 (in segments) all gradients 169 and 205, 2x16x512x32 50 and 68.
+// transpose of the forward walk's A).  All gradients, side by side and one after the
+// other: bf16 4x16x4096x64 588 and 679 us, fp32 2x8x4096x32 (in segments) 168 and 205, 2x16x512x32 50 and 68.
 template <typename E, int DK>
 cudaError_t walks(const Problem& p, const Gradients& gr, char* ws, const Space& s, cudaStream_t st) {
     constexpr int NG = sizeof(E) == 2 ? 2 : 1;

@@ -112,8 +112,8 @@ cudaError_t run(const Problem& p, const FoldArgs& a, cudaStream_t st) {
 
 // A block of one walk beside a block of the other on an SM costs both as much as one after the other,
 // a block of twice the columns only a quarter more: 64 columns where both walks' blocks then have an SM
-// each and blocks of 32 would not.  4x16x4096x64: the walks one after the other 314 us, side by side 342
-// with 32 columns and 222 with 64.
+// each and blocks of 32 would not.  4x16x4096x64, all gradients: the walks one after the other 679 us, side by
+// side 735 with 32 columns and 588 with 64.
 int gradient_columns(const Problem& p, long long walked) {
     if (!p.bf16) return 16;
     const long long walks = 2 * walked;
@@ -133,13 +133,13 @@ bool gradient_walks_beside(const Problem& p, long long blocks) {
 // as often as the heads' column slices fill the SMs (two blocks an SM where they fit, a step of which
 // takes 1.25 times one block's); with them, the summaries' walk (no outputs: about 0.85 of a step, two
 // blocks an SM), the fold (0.5 a segment at d = 64) and the second walk.  Taken when a
-// tenth is gained.  Forward at bf16, without and with the segments that it takes: 1x4x16384x64 578 and
-// 108 us, 1x8x4096x64 154 and 62, 2x16x4096x64 168 and 157; 4x16x4096x64 fills the machine: 188
-// without, 254 with three.
+// tenth is gained.  Forward at bf16, without and with the segments that it takes: 1x4x16384x64 612 and
+// 102 us, 1x8x4096x64 161 and 58, 2x16x4096x64 178 and 160; 4x16x4096x64 fills the machine: 196
+// without, 273 with.
 // The gradients have two such walks side by side, a reverse step 1.3; on SMs of their own that is all,
 // with 64 columns a block 1.25 times it, on shared ones 1.35 a wave (between 1.2 and 1.75 eight shapes
-// of ten chose the same, the two others best here): 2x16x4096x64 needs no segments, 371 us with the rest of
-// the gradients, not 424.
+// of ten chose the same, the two others best here): 2x16x4096x64 needs no segments, 367 us with the rest of
+// the gradients, not 423.
 Segments segments(const Problem& p, bool gradients) {
     const long long BH = static_cast<long long>(p.B) * p.H;
     const int NC = (p.T + C - 1) / C, CS = p.bf16 ? 32 : 16, fit = p.bf16 ? (p.d <= 64 ? 2 : 1) : (p.d == 32 ? 2 : 1);

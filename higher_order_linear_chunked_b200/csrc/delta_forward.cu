@@ -55,14 +55,15 @@ struct Cfg {
     static constexpr bool BF = sizeof(E) == 2;
     static constexpr int KT = BF ? 1 : 3;             // terms of q, k
     // terms of S0, U and P in the outputs: fp32's 24 bits for either type, since an output may be far
-    // smaller than its terms (two terms, 16 bits, measured 184 us and not 194 for 4x16x4096x64 bf16)
+    // smaller than its terms (with two, 16 bits, 4x16x4096x64 bf16 took 184 us, not 194, and 2x16x4096x128
+    // 230, not 265)
     static constexpr int OT = 3;
     static constexpr int INV = GR ? 2 : 1;
     static constexpr int AHEAD = BF ? 2 : 1;          // chunks between a tile's request and its use
     static constexpr int NLD = BF ? 2 : 4;            // loader warps (fp32 tiles are split on the way)
     // state warps of 16 columns: one holds 64 keys' part of the state and the chunk's terms in its
     // registers (bf16: 4x16x4096x64 the same with one and two, with half the warps); twice the keys, or
-    // the six products of fp32 terms, are worth the exchanges (2x16x4096x128: two 234 us, four 240)
+    // the six products of fp32 terms, are worth the exchanges (2x16x4096x128: four are 3% slower than two)
     static constexpr int NH = DK_ == 128 || (!BF && DK_ == 64) ? 2 : 1;
     static constexpr int W_STATE = NH * NG_, W_OUT = MODE_ == OUT ? NG_ : 0;
     static constexpr int WARPS = W_STATE + W_OUT + NLD;

@@ -2,11 +2,11 @@
 //     M = strict_low(D o K K^T),  P = scale low(D o Q K^T),  X = (I + M diag(beta))^-1
 // and, for the gradients, X' = (I + diag(beta) M)^-1; written to the chunk's record with its gate
 // values, as the shared-memory images that the walks copy.  All chunks of all heads are independent
-// here.  8192 chunks (4x16x4096x64, bf16) read 67 MB and write 88 MB, 155 for the gradients: 37 and 58
-// us, 65% and 59% of the copy rate; what is left is a chunk's own chain of products, substitution and
+// here.  8192 chunks (4x16x4096x64, bf16) read 67 MB and write 105 MB, 155 for the gradients: 41 and 57
+// us, 64% and 60% of the copy rate; what is left is a chunk's own chain of products, substitution and
 // copies at the ten to eighteen warps an SM that shared memory lets in.  Forward, one warp takes P and
 // another X; for the gradients one warp takes all three in turn, each in the place of what it no
-// longer needs (58 us; two warps with the larger footprint 70).
+// longer needs (57 us; two warps with the larger footprint 70).
 #include "delta_walk.cuh"
 
 namespace hla {
