@@ -3,7 +3,8 @@
 A thin ctypes binding over the C ABI of ``libhla.so`` (declared in
 ``include/hla.h``).  This module only marshals arguments: every step of the
 computation runs in the library's CUDA kernels, on the tensors' device, on the
-current torch stream.  PyTorch supplies device memory and streams.  There is no
+current torch stream or the one given as ``stream`` (what a call allocates then
+comes from that stream's memory).  PyTorch supplies device memory and streams.  There is no
 CPU implementation here and no fallback: if the library is missing or the
 tensors are not CUDA tensors, the calls raise.
 
@@ -161,6 +162,21 @@ def _check_workspace(workspace, device):
         raise ValueError("workspace must be contiguous")
 
 
+def _empty(stream, size, dtype, device, result: bool = False):
+    """What a call works in or returns, from the memory of the stream that uses it: a block of the current
+    stream's memory may still be in use by work queued there.  A result is kept for the current stream too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=device)
+    if result:
+        current = torch.cuda.current_stream(device)
+        if stream != current:
+            t.record_stream(current)
+    return t
+
+
 def workspace_bytes(op: int, dtype_code: int, decayed: bool, B: int, H: int, T: int, d: int, dv: int) -> int:
     return int(load_library().hla_workspace_bytes(op, dtype_code, int(bool(decayed)), B, H, T, d, dv))
 
@@ -181,14 +197,15 @@ def set_segment_chunks(chunks: int) -> None:
         raise HLAError(rc, "hla_set_segment_chunks")
 
 
-def make_workspace(op: int, q, v, decayed: bool = False):
-    """Allocate (with torch, on q's device) a workspace sized for this call."""
+def make_workspace(op: int, q, v, decayed: bool = False, stream=None):
+    """Allocate (with torch, on q's device, from the memory of ``stream`` if one is given) a workspace
+    sized for this call."""
     torch = _torch()
     B, H, T, d = q.shape
     n = workspace_bytes(op, _dtype_code(q), decayed, B, H, T, d, v.shape[-1])
     if n == 0:
         raise HLAError(5, "unsupported shape/dtype for this op")
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return _empty(stream, n, torch.uint8, q.device)
 
 
 def _call(op: int, q, k, v, gamma=None, eps: float = 1e-6, out=None, workspace=None, stream=None):
@@ -198,12 +215,12 @@ def _call(op: int, q, k, v, gamma=None, eps: float = 1e-6, out=None, workspace=N
     B, H, T, d = q.shape
     dv = v.shape[-1]
     if out is None:
-        out = torch.empty((B, H, T, dv), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, H, T, dv), torch.float32, q.device, result=True)
     if gamma is not None:
         if not gamma.is_cuda or gamma.dtype != torch.float32 or gamma.numel() != H or not gamma.is_contiguous():
             raise ValueError("gamma must be a contiguous CUDA float32 tensor of shape [H]")
     if workspace is None:
-        workspace = make_workspace(op, q, v, decayed=gamma is not None)
+        workspace = make_workspace(op, q, v, decayed=gamma is not None, stream=stream)
     else:
         _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -282,12 +299,10 @@ def _backward(op, q, k, v, dout, workspace, stream, eps):
     if n == 0:
         raise HLAError(5, "no backward kernel for this shape/dtype")
     if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, n, torch.uint8, q.device)
     else:
         _check_workspace(workspace, q.device)
-    dq = torch.empty((B, H, T, d), dtype=torch.float32, device=q.device)
-    dk = torch.empty_like(dq)
-    dv = torch.empty((B, H, T, dvd), dtype=torch.float32, device=q.device)
+    dq, dk, dv = (_empty(stream, (B, H, T, w), torch.float32, q.device, result=True) for w in (d, d, dvd))
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
     vp = ctypes.c_void_p
     head = [vp(q.data_ptr()), vp(k.data_ptr()), vp(v.data_ptr()), vp(dout.data_ptr()), vp(dq.data_ptr()),
@@ -359,10 +374,10 @@ def forward_profiled(op_name: str, q, k, v, events, gamma=None, eps: float = 1e-
     B, H, T, d = q.shape
     dv = v.shape[-1]
     if out is None:
-        out = torch.empty((B, H, T, dv), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, H, T, dv), torch.float32, q.device, result=True)
     op = OP_CODES[op_name]
     if workspace is None:
-        workspace = make_workspace(op, q, v, decayed=gamma is not None)
+        workspace = make_workspace(op, q, v, decayed=gamma is not None, stream=stream)
     else:
         _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -428,12 +443,12 @@ def state(op_name: str, q, k, v, gamma=None, out=None, workspace=None, stream=No
         raise ValueError(f"{op_name} needs gamma")
     n = int(lib.hla_state_floats(op, int(decayed), d, dv))
     if out is None:
-        out = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, H, n), torch.float32, q.device, result=True)
     if workspace is None:
         nb = int(lib.hla_state_workspace_bytes(op, _dtype_code(q), int(decayed), B, H, T, d, dv))
         if nb == 0:
             raise HLAError(5, "unsupported shape/dtype for this op")
-        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, nb, torch.uint8, q.device)
     else:
         _check_workspace(workspace, q.device)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -462,7 +477,7 @@ def step(op_name: str, state_io, q, k, v, gamma=None, eps: float = 1e-6, out=Non
     B, H, d = q.shape
     dv = v.shape[-1]
     if out is None:
-        out = torch.empty((B, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, H, dv), torch.float32, q.device, result=True)
     st = stream if stream is not None else torch.cuda.current_stream(q.device)
     rc = load_library().hla_step(
         OP_CODES[op_name], ctypes.c_void_p(state_io.data_ptr()), ctypes.c_void_p(q.data_ptr()),

@@ -19,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from . import HLAError, HLA_BF16, HLA_F32, HLA_OK, _check_workspace, load_library as _load
+from . import HLAError, HLA_BF16, HLA_F32, HLA_OK, _check_workspace, _empty, load_library as _load
 
 LAYOUTS = {"bhtd": 0, "bthd": 1}
 ACTIVATIONS = ("none", "silu")
@@ -78,18 +78,8 @@ def _stream_of(device: int, stream) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _empty(stream, size, dtype, device):
-    """What a call works in, from the memory of the stream that uses it: a block of the current stream's
-    memory may still be in use by work queued there."""
-    if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=dtype, device=device)
-
-
 def _likes(on: int, stream, *tensors):
-    """Results shaped like the given tensors (None for None), allocated in the same way and kept for the
-    current stream too."""
+    """Results shaped like the given tensors (None for None), allocated as by :func:`_empty`."""
     if stream is None:
         return [torch.empty_like(t) if t is not None else None for t in tensors]
     current = torch.cuda.current_stream(on)
@@ -213,9 +203,7 @@ def gated_delta(q, k, v, g, beta, scale: Optional[float] = None, initial_state=N
     if state_out is not None:
         _expect("state_out", state_out, (B, H, d, dv), torch.float32, dev)
     elif return_state:
-        state_out = _empty(stream, (B, H, d, dv), torch.float32, dev)
-        if stream is not None:
-            state_out.record_stream(torch.cuda.current_stream(on))
+        state_out = _empty(stream, (B, H, d, dv), torch.float32, dev, result=True)
     code = _CODES[q.dtype]
     if workspace is None:
         n = _bytes("hla_delta_workspace_bytes", code, B, Hk, H, T, d, dv)

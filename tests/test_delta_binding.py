@@ -72,10 +72,12 @@ class Watch:
         monkeypatch.setattr(torch.cuda, "stream", Current)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: watch.stream)
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: watch.kept.append((id(t), s)))
-        monkeypatch.setattr(module, "torch", Torch())
-        monkeypatch.setattr(module, "_call", lambda *a: None)
-        monkeypatch.setattr(module, "_stream_of", lambda *a: 0)
-        monkeypatch.setattr(module, "_raw_stream", lambda device: 0)
+        monkeypatch.setattr(hla, "_torch", Torch)
+        if module is not hla:
+            monkeypatch.setattr(module, "torch", Torch())
+            monkeypatch.setattr(module, "_call", lambda *a: None)
+            monkeypatch.setattr(module, "_stream_of", lambda *a: 0)
+            monkeypatch.setattr(module, "_raw_stream", lambda device: 0)
 
     def note(self, t):
         self.made.append((t, self.stream))
@@ -106,6 +108,25 @@ def test_what_a_call_on_a_given_stream_allocates(name, monkeypatch):
         watch.made.clear(), watch.kept.clear()
         call()
         assert watch.made and all(s is watch.current for _, s in watch.made) and not watch.kept
+
+
+@pytest.mark.parametrize("name,results", [("hla2", 1), ("hla2_normalized", 1), ("ahla", 1), ("hla3", 1), ("hla2_unmasked", 1),
+                                          ("hla2_backward", 3), ("ahla_backward", 3), ("state", 1), ("step", 1),
+                                          ("forward_profiled", 1)])
+def test_what_the_other_calls_allocate(name, results, monkeypatch):
+    """The same of the HLA family's calls (which refuse these tensors, all at address 0, once they have allocated)."""
+    with FakeTensorMode():
+        x = [fake(1, 2, 8, 64) for _ in range(3)]
+        args = {"hla2_backward": (*x, x[2]), "ahla_backward": (*x, x[2]), "state": ("hla2", *x), "forward_profiled": ("hla2", *x, ()),
+                "step": ("hla2", fake(1, 2, 17000), *(t[:, :, 0].contiguous() for t in x))}.get(name, x)
+        watch = Watch(monkeypatch, hla)
+        for stream in (watch.side, None):
+            watch.made.clear(), watch.kept.clear()
+            with pytest.raises(hla.HLAError):
+                getattr(hla, name)(*args, stream=stream)
+            want = watch.side if stream else watch.current
+            assert len(watch.made) >= results and all(s is want for _, s in watch.made)
+            assert len(watch.kept) == (results if stream else 0) and all(s is watch.current for _, s in watch.kept)
 
 
 def test_the_module_is_an_attribute_of_the_package():

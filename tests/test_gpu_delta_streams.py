@@ -28,3 +28,26 @@ def test_memory_freed_with_work_queued():
         torch.cuda.synchronize()
         assert torch.equal(o, want) and torch.equal(last, S)
         assert all(torch.equal(a, b) for a, b in zip(got[:5], grads[:5]))
+
+
+@pytest.mark.parametrize("op", ["hla2n", "ahla", "hla3"])
+def test_memory_freed_with_work_queued_hla(op):
+    """The same of the HLA family's calls; a workspace freed while its call is still queued."""
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = ((torch.randn(2, 4, 1024, 64, generator=gen) / 8).bfloat16().to(DEV) for _ in range(3))
+    want = hla.forward(op, q, k, v)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        late = torch.empty_like(want)
+        torch.cuda._sleep(40_000_000)
+        late.fill_(7.0)
+        block = late.data_ptr()
+        del late
+        side.wait_stream(torch.cuda.current_stream())           # the call is queued, not yet running
+        o = hla.forward(op, q, k, v, stream=side)
+        assert o.data_ptr() != block
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in (1 << 16, 1 << 20, 1 << 22, 1 << 24)]
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+        del junk
