@@ -67,3 +67,38 @@ def test_a_state_that_is_not_finite():
     other = [c for c in range(64) if c != 9]
     assert torch.equal(o[..., other], ref[..., other]) and torch.equal(last[..., other], S[..., other])
     assert not bool(torch.isfinite(o[..., 9]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,dv", [(32, 128), (64, 64), (128, 64)])
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+def test_many_bad_values(dtype, d, dv, layout):
+    """NaN in v at scattered places, another first token in every column (both halves of a chunk, several in
+    one column), a bad key behind them and NaN behind the end of one sequence."""
+    B, H, T = 3, 2, 100
+    x = leaves(dtype, B, 1, H, T, d, dv, seed=d + dv, state=True)
+    lens = torch.tensor([100, 61, 100], dtype=torch.int32)
+    gen = torch.Generator().manual_seed(d)
+    first = torch.full((B, H, dv), T)
+    spoilt = x[2].clone()
+    for b in range(B):
+        for h in range(H):
+            for c in range(dv):
+                ts = torch.randint(0, T, (int(torch.randint(0, 4, (1,), generator=gen)),), generator=gen)
+                spoilt[b, h, ts, c] = math.nan if c % 2 else -math.inf
+                if len(ts):
+                    first[b, h, c] = int(ts.min())
+    key = x[1].clone()
+    key[2, 0, 77, 3] = math.nan
+    first[2] = first[2].clamp(max=77)
+    put = lambda t: (t.transpose(1, 2).contiguous() if layout == "bthd" else t).to(DEV)  # noqa: E731
+    how = dict(initial_state=x[5].to(DEV), lengths=lens.to(DEV), layout=layout)
+    ref = hla.gated_delta(put(x[0]), put(x[1]), put(x[2]), put(x[3]), put(x[4]), **how)
+    o = hla.gated_delta(put(x[0]), put(key), put(spoilt), put(x[3]), put(x[4]), **how)
+    if layout == "bthd":
+        ref, o = ref.transpose(1, 2), o.transpose(1, 2)
+    t = torch.arange(T)[None, None, :, None]
+    live = t < lens[:, None, None, None]
+    hit = (t >= first[:, :, None, :]) & live
+    assert torch.equal(~torch.isfinite(o.cpu()), hit)
+    assert torch.equal(o.cpu()[~hit], ref.cpu()[~hit])
