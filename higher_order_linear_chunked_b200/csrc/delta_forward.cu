@@ -14,8 +14,6 @@
 // sequence is cut into segments (delta_fold.cu): a first walk takes each segment from a zero state and
 // also takes the unit matrix through it without values, which gives S_end = A S_start + B; the states
 // between the segments follow from those, and the second walk has all segments at once.
-#include <type_traits>
-
 #include "delta_walk.cuh"
 
 namespace hla {
@@ -38,12 +36,6 @@ struct WalkArgs {
     int Hk, H, T, dv, bthd;
     int segments, seg_chunks; // chunks of a segment
     float scale;
-};
-
-// From which token of a chunk (of a half of it, with two state warps) the columns of a group are NaN.
-struct Bad {
-    int any, pad[3];
-    int first[16];
 };
 
 // GR: the records have the gradients' form.
@@ -88,37 +80,17 @@ struct Cfg {
     static constexpr int ex = uf + (MODE_ == OUT ? 2 * UB : 0);
     static constexpr int yf = ex + (NH > 1 ? W_STATE * 2048 : 0);    // Y of the chunk as an A operand; the decayed U
     static constexpr int YB = 2 * 3 * 512;            // takes the partial sums' place
-    static constexpr int bf = yf + (NH > 1 ? NG_ * YB : 0);           // of the last two chunks for the outputs
-    static constexpr int bytes = bf + (MODE_ == OUT ? 2 * W_STATE * static_cast<int>(sizeof(Bad)) : 0);
+    static constexpr int bytes = yf + (NH > 1 ? NG_ * YB : 0);
     // of an SM; summaries of narrow bf16 heads are four warps and 38 kB, so that 128 registers a thread let
     // four share one (1x4x16384x64: 110 us, with three 126)
     static constexpr int BLOCKS = MODE_ == SUMMARY && BF && DK_ <= 64 ? 4 : bytes <= 113 * 1024 ? 2 : 1;
 };
 
-// The first bad token of a warp's writes beta R, column by column, for the outputs.
-template <int N>
-__device__ __forceinline__ void tell(Bad* to, const float (&r)[N][4], const float2 (&beta)[N], int lane) {
-    float u[N][4];
-    int first[2];
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[n][j] = r[n][j] * ((j & 1) ? beta[n].y : beta[n].x);
-    first_bad(u, lane, first);
-    if ((lane & 3) == 0) {
-        to->first[lane >> 2] = first[0];
-        to->first[8 + (lane >> 2)] = first[1];
-    }
-}
-
 // Two neighbouring tiles of S0 or U, transposed as the state warps hold them, as a B operand.
-template <bool CLEAN, int N>
-__device__ __forceinline__ void operand(const float4* from, uint32_t (&b)[N][4]) {
-    const float4 x = from[0], y = from[32];
-    float w[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
-    if constexpr (CLEAN) clean(w);
+template <int N>
+__device__ __forceinline__ void operand(const float (&x)[4], const float (&y)[4], uint32_t (&b)[N][4]) {
     uint32_t a[N][4];
-    split_a<N>(w[0], w[1], a);
+    split_a<N>(x, y, a);
 #pragma unroll
     for (int t = 0; t < N; ++t) {
         b[t][0] = a[t][0]; b[t][1] = a[t][2]; b[t][2] = a[t][1]; b[t][3] = a[t][3];
@@ -195,7 +167,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 #pragma unroll
                 for (int n = 0; n < DH / 8; ++n) sf[n * 32] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
             }
-            Bad* const bf = reinterpret_cast<Bad*>(sm + F::bf) + (c & 1) * F::W_STATE + warp;
             if (MODE == STORE) {
                 const int chunk = t_first / C + c;
                 if (chunk % a.block_chunks == 0) {
@@ -259,16 +230,12 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
 #pragma unroll
                 for (int n = 0; n < 4; ++n) be[n] = *reinterpret_cast<const float2*>(&G->beta[8 * n + 2 * (lane & 3)]);
                 if constexpr (MODE == OUT) {
-                    // found while the products are under way; then once more, cleaned
-                    const bool spoilt = any_bad(y) || G->bad != 0.f;
-                    if (lane == 0) bf->any = spoilt;
-                    if (spoilt) {
+                    if (any_bad(y)) {              // found while the products are under way; then once more, cleaned
                         int first[2];
                         first_bad(y, lane, first);
                         clean(y);
                         solve();
                         spoil(r, lane, first);
-                        tell(bf, r, be, lane);
                     }
                 }
                 if (MODE == STORE) {
@@ -419,9 +386,7 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                 }
             }
             if constexpr (MODE == OUT) {
-                const bool spoilt = any_bad(u) || G->bad != 0.f;
-                if (lane == 0) bf->any = spoilt;
-                if (spoilt) {
+                if (any_bad(z)) {
                     // once more with this half's share cleaned; the other half's stays as it is, since all of this
                     // half comes behind what is bad there
                     int first[2];
@@ -431,7 +396,6 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
                     else split_a<3>(z[0], z[1], ay[1]);
                     solve();
                     spoil(u, lane, first);
-                    tell(bf, u, beta, lane);
                 }
             }
             // U^T for the outputs, and U^T e^(c_C - c) for the state
@@ -499,55 +463,65 @@ __global__ void __launch_bounds__(F::WARPS * 32, F::BLOCKS) k_delta_walk(const W
             const float4* sf = reinterpret_cast<const float4*>(sm + F::sf + (c & 1) * F::SB) + g * (DK / 8) * 32 + lane;
             const float4* uf = reinterpret_cast<const float4*>(sm + F::uf + (c & 1) * F::UB) + g * 4 * 32 + lane;
             float acc[2][2][4] = {};          // [16 tokens][8 columns]
-            const auto chunk = [&](auto with_bad) {
+            float U[4][4];
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    uint32_t aq[2][KT][4], bs[1][OT][4];
-                    operand<false>(sf + 2 * ks * 32, bs[0]);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-#pragma unroll
-                        for (int t = 0; t < KT; ++t) ldsm4(aq[m][t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2) + m * 16 * DK * 2);
-                        prod<KT, OT, 1>(acc[m], aq[m], bs);
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float f[2] = {a.scale * G->since[16 * m + (lane >> 2)], a.scale * G->since[16 * m + 8 + (lane >> 2)]};
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[m][n][j] *= f[j >> 1];
-                }
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t ap[OT][4], bu[1][OT][4];
-                    operand<decltype(with_bad)::value>(uf + 2 * kk * 32, bu[0]);
-#pragma unroll
-                    for (int m = kk; m < 2; ++m) {     // P is lower triangular
-#pragma unroll
-                        for (int t = 0; t < OT; ++t) ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2) + m * 16 * C * 2);
-                        prod<OT, OT, 1>(acc[m], ap, bu);
-                    }
+            for (int n = 0; n < 4; ++n) load4(reinterpret_cast<const float*>(uf + n * 32), U[n]);
+            // bad writes are cleaned, and the outputs from their tokens on spoilt below; looked for where it measured
+            // faster (behind the state's products 195 and 277 us at 4x16x4096x64 and 2x16x4096x128, before them 198 and 269)
+            bool spoilt;
+            int first[2];
+            const auto look = [&] {
+                spoilt = any_bad(U);
+                if (spoilt) {
+                    first_bad(U, lane, first);
+                    clean(U);
                 }
             };
-            const Bad* const bf = reinterpret_cast<const Bad*>(sm + F::bf) + (c & 1) * F::W_STATE + g * NH;
-            if ((bf[0].any | bf[NH - 1].any) == 0) {
-                chunk(std::false_type{});
-            } else {
-                chunk(std::true_type{});
+            if (DK == 128) look();
 #pragma unroll
-                for (int part = 0; part < NH; ++part)
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                uint32_t aq[2][KT][4], bs[1][OT][4];
+                float x[2][4];
+                load4(reinterpret_cast<const float*>(sf + 2 * ks * 32), x[0]);
+                load4(reinterpret_cast<const float*>(sf + (2 * ks + 1) * 32), x[1]);
+                operand<OT>(x[0], x[1], bs[0]);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int m = 0; m < 2; ++m) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            int first = bf[part].any ? bf[part].first[8 * n + 2 * (lane & 3) + (j & 1)] : C;
-                            if (NH > 1) first = first < 16 ? first + 16 * part : C;
+                    for (int t = 0; t < KT; ++t) ldsm4(aq[m][t], ((q_a + so) ^ (ks << 5)) + t * (C * DK * 2) + m * 16 * DK * 2);
+                    prod<KT, OT, 1>(acc[m], aq[m], bs);
+                }
+            }
+            if (DK < 128) look();
 #pragma unroll
-                            for (int m = 0; m < 2; ++m)
-                                if (16 * m + (lane >> 2) + 8 * (j >> 1) >= first) acc[m][n][j] = __int_as_float(0x7fffffff);
-                        }
+            for (int m = 0; m < 2; ++m) {
+                const float f[2] = {a.scale * G->since[16 * m + (lane >> 2)], a.scale * G->since[16 * m + 8 + (lane >> 2)]};
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[m][n][j] *= f[j >> 1];
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                uint32_t ap[OT][4], bu[1][OT][4];
+                operand<OT>(U[2 * kk], U[2 * kk + 1], bu[0]);
+#pragma unroll
+                for (int m = kk; m < 2; ++m) {     // P is lower triangular
+#pragma unroll
+                    for (int t = 0; t < OT; ++t) ldsm4(ap[t], ((p_a + so) ^ (kk << 5)) + t * (C * C * 2) + m * 16 * C * 2);
+                    prod<OT, OT, 1>(acc[m], ap, bu);
+                }
+            }
+            if (spoilt) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {            // the column's first bad token, from the lanes that have it
+                        const int from = __shfl_sync(0xffffffffu, first[n], 4 * (2 * (lane & 3) + (j & 1)));
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            if (16 * m + (lane >> 2) + 8 * (j >> 1) >= from) acc[m][n][j] = __int_as_float(0x7fffffff);
+                    }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

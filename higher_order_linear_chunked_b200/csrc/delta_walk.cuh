@@ -56,8 +56,7 @@ constexpr int kMS = 36;                      // floats of a row of the transpose
 struct Gates {
     float since[C], left[C], beta[C];
     float all;
-    float bad;               // not 0: a beta is infinite or NaN
-    float pad[30];
+    float pad[31];
 };
 static_assert(sizeof(Gates) == 512, "a record's last piece");
 
@@ -191,9 +190,7 @@ __device__ __forceinline__ void finish_gates(Gates* s, float2* sum, float g, flo
     s->since[lane] = since;
     s->left[lane] = ex2_long(last - c);
     s->beta[lane] = beta;
-    s->pad[lane < 30 ? lane : 29] = 0.f;
-    const bool any = __any_sync(0xffffffffu, bad(beta));
-    if (lane == 0) s->bad = any ? 1.f : 0.f;
+    s->pad[lane < 31 ? lane : 30] = 0.f;
     if (lane == 31) s->all = since;
 }
 

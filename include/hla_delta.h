@@ -30,10 +30,10 @@
  * Values.  g below -120 (-inf too) counts as -120, whose exp is zero in fp32, and so starts the head
  * anew at that token.  Positive g are allowed while their sums over 64 neighbouring tokens stay below
  * 88 (exp of it is the largest fp32); decays (g <= 0) always do.
- * A NaN or an infinity in a live token leaves the outputs of the tokens before it as they are without it, and
- * one in v the outputs and the state of the other columns; from there on everything is NaN (one in q: that
- * token's output only).  fp32 values are to stay below bf16's largest, 3.39e38.  Gradients: everything of that value head, and of its key head,
- * may be NaN then.
+ * A NaN or an infinity in a live token, or one that the recurrence comes to there, leaves the outputs of the
+ * tokens before it as they are without it, and one in v the outputs and the state of the other columns;
+ * from there on everything is NaN (one in q: that token's output only).  fp32 values are to stay below bf16's
+ * largest, 3.39e38.  Gradients: everything of that value head, and of its key head, may be NaN then.
  */
 #ifndef HLA_DELTA_H_
 #define HLA_DELTA_H_

@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import higher_order_linear_chunked_b200 as hla  # noqa: E402
+from oracle import delta as od  # noqa: E402
 from test_gpu_delta import DEV, leaves  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +103,21 @@ def test_many_bad_values(dtype, d, dv, layout):
     hit = (t >= first[:, :, None, :]) & live
     assert torch.equal(~torch.isfinite(o.cpu()), hit)
     assert torch.equal(o.cpu()[~hit], ref.cpu()[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_an_overflow_stays_out_of_earlier_tokens(dtype, d):
+    """Keys of squared length 40 multiply the state by -39 a token, which overflows behind the 23rd: what
+    stands before is what the same call over fewer tokens gives."""
+    x = leaves(dtype, 1, 1, 1, 60, d, 32, seed=d, state=False)[:5]
+    x[1][:] = math.sqrt(40) * x[1][:, :, :1].clone()
+    x[3][:], x[4][:] = 0.0, 1.0
+    want, S = od.forward(*x[:5], 1.0)
+    dev = [t.to(DEV) for t in x]
+    full = hla.gated_delta(*dev, scale=1.0)
+    assert not bool(torch.isfinite(full[:, :, 40:]).any())
+    for n in (3, 17, 21):
+        assert float(want[:, :, :n].abs().max()) < 1e36
+        part = hla.gated_delta(*dev, scale=1.0, lengths=torch.tensor([n], dtype=torch.int32, device=DEV))
+        assert bool(torch.isfinite(part).all()) and torch.equal(full[:, :, :n], part[:, :, :n])
